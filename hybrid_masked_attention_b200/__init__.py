@@ -11,7 +11,9 @@ Function names mirror the C entry points:
     attn_target_cached_fwd, attn_target_cached,
     bwd_workspace_bytes, attn_full_bwd, attn_target_bwd, attn_target_bwd_static,
     stack_workspace_bytes, layer_fwd, stack_fwd, v2_workspace_bytes, v2_target_layer_fwd,
-    selftest_wait_timeout
+    selftest_wait_timeout,
+    add_rmsnorm_fp8, rmsnorm_bwd_workspace_bytes, rmsnorm_bwd, gate_fwd_fp8, fp8_quant, fp8_gemm, fp8_check,
+    fp8_stack_workspace_bytes, fp8_layer_fwd, fp8_stack_fwd
 """
 from __future__ import annotations
 
@@ -102,7 +104,19 @@ class CV2LayerWeights(ctypes.Structure):
                 ("w_down", ctypes.c_void_p * 4)]
 
 
+class CFp8Weight(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scale", ctypes.c_void_p), ("ld_scale", ctypes.c_int64)]
+
+
+class CFp8LayerWeights(ctypes.Structure):
+    _fields_ = [("rms_w", ctypes.c_void_p), ("w_in", CFp8Weight), ("w_kv", CFp8Weight), ("w_o", CFp8Weight),
+                ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
+_I = ctypes.c_int32
+_L = ctypes.c_int64
+_F8LWP = ctypes.POINTER(CFp8LayerWeights)
 _CP = ctypes.POINTER(CCfg)
 _LWP = ctypes.POINTER(CLayerWeights)
 _V2P = ctypes.POINTER(CV2LayerWeights)
@@ -136,6 +150,19 @@ _sigs = {
     "mtfm_layer_fwd": (ctypes.c_int, [_CP, _P, ctypes.c_int32, ctypes.c_int, _LWP, _P, _P, ctypes.c_size_t, _P]),
     "mtfm_stack_fwd": (ctypes.c_int, [_CP, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_char_p, _LWP, _P, _P,
                                       ctypes.c_size_t, _P]),
+    "mtfm_add_rmsnorm_fp8": (ctypes.c_int, [_I, _I, _P, _I, _L, _P, _I, _L, _P, ctypes.c_float, _P, _L, _P, _L, _P, _L,
+                                            _P, _P]),
+    "mtfm_rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _I]),
+    "mtfm_rmsnorm_bwd": (ctypes.c_int, [_I, _I, _P, _I, _L, _P, _P, _P, _I, _L, _P, _I, _L, _P, _L, _P, _P,
+                                        ctypes.c_size_t, _P]),
+    "mtfm_gate_fwd_fp8": (ctypes.c_int, [_CP, _P, ctypes.c_int, _P, _P, _P, _P, _P, _L, _P, _L, _P, _P]),
+    "mtfm_fp8_quant": (ctypes.c_int, [_I, _I, _P, _I, _L, _I, _P, _L, _P, _L, _P]),
+    "mtfm_fp8_gemm": (ctypes.c_int, [_I, _I, _I, _P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _L, _P, _I, _L, _P, _P]),
+    "mtfm_fp8_check": (ctypes.c_int, [_P, _P]),
+    "mtfm_fp8_stack_workspace_bytes": (ctypes.c_size_t, [_CP, ctypes.c_int32]),
+    "mtfm_fp8_layer_fwd": (ctypes.c_int, [_CP, _P, ctypes.c_int32, ctypes.c_int, _F8LWP, _P, _P, ctypes.c_size_t, _P]),
+    "mtfm_fp8_stack_fwd": (ctypes.c_int, [_CP, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_char_p, _F8LWP, _P, _P,
+                                          ctypes.c_size_t, _P]),
 }
 for _name, (_res, _args) in _sigs.items():
     _f = getattr(_lib, _name)
@@ -534,3 +561,240 @@ def selftest_wait_timeout(meta: torch.Tensor, limit_cycles: int = 2_000_000, str
     _check(_lib.mtfm_selftest_wait_timeout(_ptr(meta, torch.uint8, name="meta"), int(limit_cycles),
                                            _stream(stream)), "mtfm_selftest_wait_timeout")
 
+
+# ---------------------------------------------------------------------------- 8-bit projections
+#
+# An 8-bit matrix is a pair (values float8_e4m3fn [rows, cols], scale fp32): one scale per 128
+# columns of a row, or per 128 x 128 block of a weight (see mtfm.h).  Matrices are 2-D with
+# unit column stride; rows may lie further apart than their columns.  Every tensor of a call
+# is on one device, and the call runs on a stream of that device (the current one of it by
+# default), whichever device is current.
+
+_F8 = torch.float8_e4m3fn
+_F32 = torch.float32
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_ACTS = {None: 0, "silu": 1}
+FP8_GROUP = 128
+
+
+def _groups(n: int) -> int:
+    return -(-n // FP8_GROUP)
+
+
+def _mat(t, name, dev, rows, cols, dtype=None):
+    """(pointer, pitch) of a [rows, cols] matrix of `dtype` (None: fp32 or bf16) on `dev`."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}, got {t.device}")
+    if t.dtype != dtype and (dtype is not None or t.dtype not in _TYPES):
+        raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if rows > 1 and ld < cols:
+        raise ValueError(f"{name} has overlapping rows (pitch {ld} for {cols} columns)")
+    return t.data_ptr(), ld
+
+
+def _vec(t, name, dev, n, dtype=_F32):
+    if t.device != dev or t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {dev}")
+    return t.data_ptr()
+
+
+def _cuda_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    return t.device
+
+
+def _run_on(dev, stream, where, fn, *args):
+    """Calls fn(*args, stream) with `dev` current; stream None: the device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    if st != MTFM_OK:
+        raise MtfmError(st, where)
+
+
+def add_rmsnorm_fp8(x, delta, weight, x_out, out, scale, rstd=None, eps=0.0, stream=None):
+    """h = x + delta; x_out = h in x's type; (out, scale) = 8-bit groups of RMSNorm(h) * weight.
+
+    x fp32 or bf16 [rows, dim]; delta fp32 or bf16, or None (then x_out is None); x_out may be x,
+    or None; weight fp32 [dim]; out float8_e4m3fn [rows, dim]; scale fp32 [rows, ceil(dim / 128)];
+    rstd fp32 [rows] or None; eps <= 0 selects 1e-6."""
+    dev = _cuda_device(x, "x")
+    rows, dim = x.shape
+    px, ldx = _mat(x, "x", dev, rows, dim)
+    pd, ldd = (None, 0) if delta is None else _mat(delta, "delta", dev, rows, dim)
+    po, ldo = (None, 0) if x_out is None else _mat(x_out, "x_out", dev, rows, dim, x.dtype)
+    pq, ldq = _mat(out, "out", dev, rows, dim, _F8)
+    ps, lds = _mat(scale, "scale", dev, rows, _groups(dim), _F32)
+    _run_on(dev, stream, "mtfm_add_rmsnorm_fp8", _lib.mtfm_add_rmsnorm_fp8, rows, dim, px, _TYPES[x.dtype], ldx, pd,
+            0 if delta is None else _TYPES[delta.dtype], ldd, _vec(weight, "weight", dev, dim), eps, po, ldo, pq, ldq, ps,
+            lds, None if rstd is None else _vec(rstd, "rstd", dev, rows))
+
+
+def rmsnorm_bwd_workspace_bytes(rows: int, dim: int) -> int:
+    n = _lib.mtfm_rmsnorm_bwd_workspace_bytes(rows, dim)
+    if n == 0:
+        raise MtfmError(3, "mtfm_rmsnorm_bwd_workspace_bytes")
+    return n
+
+
+def rmsnorm_bwd(x, weight, rstd, dy, dres, dx, dw, ws, stream=None):
+    """Gradients of RMSNorm(x) * weight: dx = norm's gradient of dy, plus dres (or None); dw [dim].
+
+    x: the normalised stream (add_rmsnorm_fp8's x_out) with its rstd; dx has x's type and may be dy
+    or dres; ws: uint8 of rmsnorm_bwd_workspace_bytes(rows, dim), not shared by overlapping calls."""
+    dev = _cuda_device(x, "x")
+    rows, dim = x.shape
+    px, ldx = _mat(x, "x", dev, rows, dim)
+    py, ldy = _mat(dy, "dy", dev, rows, dim)
+    pr, ldr = (None, 0) if dres is None else _mat(dres, "dres", dev, rows, dim)
+    pd, ldd = _mat(dx, "dx", dev, rows, dim, x.dtype)
+    _run_on(dev, stream, "mtfm_rmsnorm_bwd", _lib.mtfm_rmsnorm_bwd, rows, dim, px, _TYPES[x.dtype], ldx,
+            _vec(weight, "weight", dev, dim), _vec(rstd, "rstd", dev, rows), py, _TYPES[dy.dtype], ldy, pr,
+            0 if dres is None else _TYPES[dres.dtype], ldr, pd, ldd, _vec(dw, "dw", dev, dim),
+            _vec(ws, "ws", dev, ws.numel(), torch.uint8), ws.numel())
+
+
+def gate_fwd_fp8(cfg, meta, target: bool, a, u, gamma, beta, out, scale, stats, stream=None):
+    """gate_fwd with its output in 8 bits: (out, scale) = groups of GLN(A) (*) U."""
+    rows, D = cfg.total_t if target else cfg.total_tokens, cfg.D
+    dev = _cuda_device(a, "a")
+    for t, name in ((meta, "meta"), (u, "u"), (gamma, "gamma"), (beta, "beta"), (stats, "stats")):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    pq, ldq = _mat(out, "out", dev, rows, D, _F8)
+    ps, lds = _mat(scale, "scale", dev, rows, _groups(D), _F32)
+    c = cfg.c()
+    _run_on(dev, stream, "mtfm_gate_fwd_fp8", _lib.mtfm_gate_fwd_fp8, ctypes.byref(c), _ptr(meta, torch.uint8, None, "meta"),
+            int(bool(target)), _ptr(a, _F32, (rows, D), "a"), _ptr(u, torch.bfloat16, (rows, D), "u"),
+            _ptr(gamma, _F32, (3, D), "gamma"), _ptr(beta, _F32, (3, D), "beta"), pq, ldq, ps, lds,
+            _ptr(stats, _F32, (rows, 2), "stats"))
+
+
+def fp8_quant(x, out, scale, block_rows: int = 1, stream=None):
+    """(out, scale) = x in 8 bits, one scale per 1 x 128 group (block_rows 1) or 128 x 128 block (128)."""
+    dev = _cuda_device(x, "x")
+    rows, cols = x.shape
+    if block_rows not in (1, FP8_GROUP):
+        raise ValueError("block_rows must be 1 or 128")
+    px, ldx = _mat(x, "x", dev, rows, cols)
+    pq, ldq = _mat(out, "out", dev, rows, cols, _F8)
+    ps, lds = _mat(scale, "scale", dev, -(-rows // block_rows), _groups(cols), _F32)
+    _run_on(dev, stream, "mtfm_fp8_quant", _lib.mtfm_fp8_quant, rows, cols, px, _TYPES[x.dtype], ldx, block_rows, pq, ldq,
+            ps, lds)
+
+
+def fp8_gemm(a, a_scale, b, b_scale, out, status, act: Optional[str] = None, residual=None, stream=None):
+    """out [m, n] = act(A B^T) + residual: A [m, k] with 1 x 128 scales, B [n, k] with 128 x 128.
+
+    act None or "silu"; out fp32 or bf16; residual None or a matrix of out's type (out itself
+    allowed); a and b start on 16-byte boundaries with row pitches that are multiples of 16;
+    status: int32 [1], zeroed once (fp8_check reads it)."""
+    dev = _cuda_device(a, "a")
+    _cuda_device(b, "b")
+    m, k = a.shape
+    n = b.shape[0]
+    if act not in _ACTS:
+        raise ValueError(f"act must be None or 'silu', got {act!r}")
+    pa, lda = _mat(a, "a", dev, m, k, _F8)
+    psa, ldsa = _mat(a_scale, "a_scale", dev, m, _groups(k), _F32)
+    pb, ldb = _mat(b, "b", dev, n, k, _F8)
+    psb, ldsb = _mat(b_scale, "b_scale", dev, _groups(n), _groups(k), _F32)
+    po, ldo = _mat(out, "out", dev, m, n)
+    pr, ldr = (None, 0) if residual is None else _mat(residual, "residual", dev, m, n, out.dtype)
+    _run_on(dev, stream, "mtfm_fp8_gemm", _lib.mtfm_fp8_gemm, m, n, k, pa, lda, psa, ldsa, pb, ldb, psb, ldsb, _ACTS[act],
+            pr, ldr, po, _TYPES[out.dtype], ldo, _vec(status, "status", dev, 1, torch.int32))
+
+
+def fp8_check(status, stream=None):
+    """Synchronises the stream; raises MtfmError if a product on this status word failed."""
+    dev = status.device
+    _run_on(dev, stream, "mtfm_fp8_check", _lib.mtfm_fp8_check, _vec(status, "status", dev, 1, torch.int32))
+
+
+@dataclass
+class Fp8LayerWeights:
+    """Device tensors of one backbone layer with 8-bit projections (``mtfm_fp8_layer_weights``):
+    LayerWeights with w_in, w_kv, w_o as pairs (float8_e4m3fn values, fp32 128 x 128 scales)."""
+    kind: str
+    rms_w: torch.Tensor
+    w_in: tuple
+    w_kv: Optional[tuple]
+    w_o: tuple
+    gamma: Optional[torch.Tensor] = None
+    beta: Optional[torch.Tensor] = None
+
+    @classmethod
+    def quantized(cls, w: LayerWeights, stream=None) -> "Fp8LayerWeights":
+        """The 8-bit form of a layer's weights (the norms' parameters are shared)."""
+        def q(t):
+            if t is None:
+                return None
+            out = torch.empty(t.shape, dtype=_F8, device=t.device)
+            scale = torch.empty(_groups(t.shape[0]), _groups(t.shape[1]), dtype=_F32, device=t.device)
+            fp8_quant(t, out, scale, FP8_GROUP, stream)
+            return out, scale
+        return cls(w.kind, w.rms_w, q(w.w_in), q(w.w_kv), q(w.w_o), w.gamma, w.beta)
+
+
+def _fp8_weight(pair, name, dev, rows, cols) -> CFp8Weight:
+    pq, ldq = _mat(pair[0], name, dev, rows, cols, _F8)
+    ps, lds = _mat(pair[1], f"{name} scale", dev, _groups(rows), _groups(cols), _F32)
+    return CFp8Weight(pq, ldq, ps, lds)
+
+
+def _fp8_layer_struct(cfg: Config, d_model: int, w: Fp8LayerWeights, dev) -> CFp8LayerWeights:
+    D, Dkv = cfg.D, cfg.Dkv
+    if w.kind not in ("F", "T"):
+        raise ValueError("layer kind must be 'F' or 'T'")
+    target = w.kind == "T"
+    if target != (w.w_kv is not None):
+        raise ValueError("w_kv is required for a Target layer and must be None for a Full layer")
+    return CFp8LayerWeights(
+        _ptr(w.rms_w, _F32, (d_model,), "rms_w"),
+        _fp8_weight(w.w_in, "w_in", dev, 2 * D if target else 2 * D + 2 * Dkv, d_model),
+        _fp8_weight(w.w_kv, "w_kv", dev, 2 * Dkv, d_model) if target else CFp8Weight(),
+        _fp8_weight(w.w_o, "w_o", dev, d_model, D),
+        _ptr(w.gamma, _F32, (3, D), "gamma"), _ptr(w.beta, _F32, (3, D), "beta"))
+
+
+def fp8_stack_workspace_bytes(cfg: Config, d_model: int) -> int:
+    c = cfg.c()
+    n = _lib.mtfm_fp8_stack_workspace_bytes(ctypes.byref(c), int(d_model))
+    if n == 0:
+        raise MtfmError(3, "mtfm_fp8_stack_workspace_bytes")
+    return n
+
+
+def fp8_layer_fwd(cfg: Config, meta, d_model: int, w: Fp8LayerWeights, x, ws, stream=None):
+    """layer_fwd with 8-bit projections: X (fp32 [total_tokens, d_model]) updated in place."""
+    c = cfg.c()
+    dev = _cuda_device(x, "x")
+    lw = _fp8_layer_struct(cfg, d_model, w, dev)
+    _run_on(dev, stream, "mtfm_fp8_layer_fwd", _lib.mtfm_fp8_layer_fwd, ctypes.byref(c), _ptr(meta, torch.uint8, name="meta"),
+            int(d_model), int(w.kind == "T"), ctypes.byref(lw), _ptr(x, _F32, (cfg.total_tokens, d_model), "x"),
+            _ptr(ws, torch.uint8, name="ws"), ws.numel())
+
+
+def fp8_stack_fwd(cfg: Config, meta, d_model: int, layers, x, ws, stream=None):
+    """Run ``layers`` (a list of Fp8LayerWeights) on X in place."""
+    c = cfg.c()
+    dev = _cuda_device(x, "x")
+    arr = (CFp8LayerWeights * max(1, len(layers)))(*[_fp8_layer_struct(cfg, d_model, w, dev) for w in layers])
+    kinds = "".join(w.kind for w in layers).encode()
+    _run_on(dev, stream, "mtfm_fp8_stack_fwd", _lib.mtfm_fp8_stack_fwd, ctypes.byref(c), _ptr(meta, torch.uint8, name="meta"),
+            int(d_model), len(layers), kinds, arr, _ptr(x, _F32, (cfg.total_tokens, d_model), "x"),
+            _ptr(ws, torch.uint8, name="ws"), ws.numel())

@@ -4,6 +4,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "fp8.cuh"
 #include "mtfm_internal.cuh"
 
 using namespace mtfm;
@@ -359,6 +360,123 @@ mtfm_status stack_fwd(const mtfm_cfg* cfg, const void* d_meta, int d, int n_laye
   return MTFM_OK;
 }
 
+// ------------------------------------------------------------------ 8-bit projections
+// Scratch of one layer with 8-bit projections: as StackWs, with X~, X~_T and Y as e4m3 and
+// their scales (one for each 128 columns of a row).
+struct Fp8StackWs {
+  size_t xn, xn_s, xnt, xnt_s, u, q, k, v, a, y, y_s, stats, total;
+};
+Fp8StackWs fp8_stack_ws(const Resolved& r, int d) {
+  Fp8StackWs w;
+  const size_t N = (size_t)r.total_tokens, T = (size_t)r.total_t;
+  const size_t gd = (d + kGroup - 1) / kGroup, gD = (r.D + kGroup - 1) / kGroup;
+  size_t o = 0;
+  w.xn = o;    o = align256(o + N * d);
+  w.xn_s = o;  o = align256(o + N * gd * 4);
+  w.xnt = o;   o = align256(o + T * d);
+  w.xnt_s = o; o = align256(o + T * gd * 4);
+  w.u = o;     o = align256(o + N * r.D * 2);
+  w.q = o;     o = align256(o + N * r.D * 2);
+  w.k = o;     o = align256(o + N * r.Dkv * 2);
+  w.v = o;     o = align256(o + N * r.Dkv * 2);
+  w.a = o;     o = align256(o + N * r.D * 4);
+  w.y = o;     o = align256(o + N * r.D);
+  w.y_s = o;   o = align256(o + N * gD * 4);
+  w.stats = o; o = align256(o + N * 2 * 4);
+  w.total = o;
+  return w;
+}
+
+// An e4m3 weight of `cols` columns in 128 x 128 blocks.
+bool fp8_weight_ok(const mtfm_fp8_weight& w, int rows, int cols) {
+  return w.data && aligned16(w.data) && w.ld >= cols && w.ld % 16 == 0 && w.scale &&
+         (reinterpret_cast<uintptr_t>(w.scale) & 3u) == 0 && (rows <= kGroup || w.ld_scale >= (cols + kGroup - 1) / kGroup);
+}
+mtfm_status check_fp8_layer_weights(const Resolved& r, int d, const mtfm_fp8_layer_weights* w, bool target) {
+  if (!w || !w->rms_w || !aligned16(w->rms_w)) return MTFM_ERR_INVALID_ARG;
+  if (target != (w->w_kv.data != nullptr)) return MTFM_ERR_INVALID_ARG;
+  if ((w->gamma == nullptr) != (w->beta == nullptr)) return MTFM_ERR_INVALID_ARG;
+  if (w->gamma && (!aligned16(w->gamma) || !aligned16(w->beta))) return MTFM_ERR_INVALID_ARG;
+  if (!fp8_weight_ok(w->w_in, target ? 2 * r.D : 2 * r.D + 2 * r.Dkv, d) || !fp8_weight_ok(w->w_o, d, r.D) ||
+      (target && !fp8_weight_ok(w->w_kv, 2 * r.Dkv, d)))
+    return MTFM_ERR_INVALID_ARG;
+  return MTFM_OK;
+}
+
+// One layer, all launches on `st`; arguments already checked.
+cudaError_t fp8_layer_fwd(const Resolved& r, const MetaView& m, const MetaLayout& L, int d, bool target,
+                          const mtfm_fp8_layer_weights& w, float* x, char* ws, const Fp8StackWs& W, cudaStream_t st) {
+  auto bf = [&](size_t off) { return reinterpret_cast<__nv_bfloat16*>(ws + off); };
+  auto out8 = [&](size_t q, size_t s, int cols) {
+    return Fp8Out{reinterpret_cast<uint8_t*>(ws + q), cols, reinterpret_cast<float*>(ws + s), (cols + kGroup - 1) / kGroup};
+  };
+  auto in8 = [&](size_t q, size_t s, int cols) {
+    const Fp8Out o = out8(q, s, cols);
+    return Fp8In{o.q, o.ld, o.scale, o.ld_scale};
+  };
+  auto wt = [](const mtfm_fp8_weight& v) { return Fp8In{v.data, v.ld, v.scale, v.ld_scale}; };
+  const int N = r.total_tokens, T = r.total_t, D = r.D, Dkv = r.Dkv;
+  const int rows_q = target ? T : N;
+  int32_t* err = &m.hdr->error;
+  const MatIn xin{x, d, MTFM_F32}, none{nullptr, 0, MTFM_F32};
+  const MatOut no_out{nullptr, 0, MTFM_F32};
+  cudaError_t e;
+  // X~ of every row (K, V read all rows), and gathered for a Target layer's T rows
+  if ((e = launch_add_rmsnorm_fp8(err, N, d, xin, none, nullptr, w.rms_w, kRmsEps, no_out, out8(W.xn, W.xn_s, d), nullptr,
+                                  st)) != cudaSuccess)
+    return e;
+  if (target && (e = launch_add_rmsnorm_fp8(err, T, d, xin, none, m.t_rows, w.rms_w, kRmsEps, no_out,
+                                            out8(W.xnt, W.xnt_s, d), nullptr, st)) != cudaSuccess)
+    return e;
+  if (!target) {
+    const Fp8Epi g{MTFM_ACT_SILU, MTFM_BF16, 4, {0, D, 2 * D, 2 * D + Dkv, 2 * D + 2 * Dkv},
+                   {bf(W.u), bf(W.q), bf(W.k), bf(W.v)}, {D, D, Dkv, Dkv}, nullptr, 0, nullptr};
+    if ((e = launch_gemm_fp8(err, N, 2 * D + 2 * Dkv, d, in8(W.xn, W.xn_s, d), wt(w.w_in), g, st)) != cudaSuccess) return e;
+  } else {
+    const Fp8Epi guq{MTFM_ACT_SILU, MTFM_BF16, 2, {0, D, 2 * D, 2 * D, 2 * D}, {bf(W.u), bf(W.q), nullptr, nullptr},
+                     {D, D, 0, 0}, nullptr, 0, nullptr};
+    if ((e = launch_gemm_fp8(err, T, 2 * D, d, in8(W.xnt, W.xnt_s, d), wt(w.w_in), guq, st)) != cudaSuccess) return e;
+    const Fp8Epi gkv{MTFM_ACT_SILU, MTFM_BF16, 2, {0, Dkv, 2 * Dkv, 2 * Dkv, 2 * Dkv}, {bf(W.k), bf(W.v), nullptr, nullptr},
+                     {Dkv, Dkv, 0, 0}, nullptr, 0, nullptr};
+    if ((e = launch_gemm_fp8(err, N, 2 * Dkv, d, in8(W.xn, W.xn_s, d), wt(w.w_kv), gkv, st)) != cudaSuccess) return e;
+  }
+  float* a = reinterpret_cast<float*>(ws + W.a);
+  if ((e = launch_attn(r, m, L, target, bf(W.q), bf(W.k), bf(W.v), a, st)) != cudaSuccess) return e;
+  if ((e = launch_gate_fwd_fp8(m, target, rows_q, D, r.eps, a, bf(W.u), w.gamma, w.beta, out8(W.y, W.y_s, D),
+                               reinterpret_cast<float*>(ws + W.stats), st)) != cudaSuccess)
+    return e;
+  // X (+)= Y W_o^T, scattered back to the T rows for a Target layer
+  const Fp8Epi go{MTFM_ACT_NONE, MTFM_F32, 1, {0, d, d, d, d}, {x, nullptr, nullptr, nullptr}, {d, 0, 0, 0}, x, d,
+                  target ? m.t_rows : nullptr};
+  return launch_gemm_fp8(err, rows_q, d, D, in8(W.y, W.y_s, D), wt(w.w_o), go, st);
+}
+
+mtfm_status fp8_stack_fwd(const mtfm_cfg* cfg, const void* d_meta, int d, int n_layers, const char* kinds,
+                          const mtfm_fp8_layer_weights* layers, float* d_x, void* d_ws, size_t ws_bytes, void* stream) {
+  Resolved r;
+  mtfm_status s = resolve(cfg, &r);
+  if (s != MTFM_OK) return s;
+  if ((s = check_meta(d_meta, r)) != MTFM_OK) return s;
+  if ((s = check_stack_cfg(r, d)) != MTFM_OK) return s;
+  if (n_layers < 0 || (n_layers > 0 && (!kinds || !layers))) return MTFM_ERR_INVALID_ARG;
+  for (int l = 0; l < n_layers; ++l) {
+    if (kinds[l] != 'F' && kinds[l] != 'T') return MTFM_ERR_INVALID_ARG;
+    if ((s = check_fp8_layer_weights(r, d, &layers[l], kinds[l] == 'T')) != MTFM_OK) return s;
+  }
+  if (n_layers == 0 || r.total_tokens == 0) return MTFM_OK;
+  const Fp8StackWs W = fp8_stack_ws(r, d);
+  if (!d_x || !aligned16(d_x)) return MTFM_ERR_INVALID_ARG;
+  if (!d_ws || (reinterpret_cast<uintptr_t>(d_ws) & 255u)) return MTFM_ERR_INVALID_ARG;
+  if (ws_bytes < W.total) return MTFM_ERR_WORKSPACE_TOO_SMALL;
+  const MetaLayout L = meta_layout(r.B, r.total_tokens, r.total_t);
+  const MetaView m = meta_view(const_cast<void*>(d_meta), L);
+  for (int l = 0; l < n_layers; ++l)
+    if (fp8_layer_fwd(r, m, L, d, kinds[l] == 'T', layers[l], d_x, static_cast<char*>(d_ws), W,
+                      static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return MTFM_ERR_CUDA;
+  return MTFM_OK;
+}
+
 // ------------------------------------------------------------------ V2 Target layer
 // Scratch: the stack's layer scratch, then the FFN's pre-normed input X~2_T (bf16
 // [T, d]) and hidden layer H (bf16 [T, d_ff]).
@@ -699,6 +817,51 @@ mtfm_status mtfm_stack_fwd(const mtfm_cfg* cfg, const void* d_meta, int32_t d_mo
                            const char* kinds, const mtfm_layer_weights* layers, float* d_x, void* d_ws,
                            size_t ws_bytes, void* stream) {
   return stack_fwd(cfg, d_meta, d_model, n_layers, kinds, layers, d_x, d_ws, ws_bytes, stream);
+}
+
+mtfm_status mtfm_gate_fwd_fp8(const mtfm_cfg* cfg, const void* d_meta, int is_target, const float* d_a,
+                              const uint16_t* d_u, const float* d_gamma, const float* d_beta, uint8_t* d_out,
+                              int64_t ld_out, float* d_scale, int64_t ld_scale, float* d_stats, void* stream) {
+  Resolved r;
+  mtfm_status s = resolve(cfg, &r);
+  if (s != MTFM_OK) return s;
+  if ((s = check_meta(d_meta, r)) != MTFM_OK) return s;
+  const int rows = is_target ? r.total_t : r.total_tokens;
+  if (rows == 0) return MTFM_OK;
+  if (!d_a || !d_u || !d_out || !d_scale) return MTFM_ERR_INVALID_ARG;
+  if ((d_gamma == nullptr) != (d_beta == nullptr)) return MTFM_ERR_INVALID_ARG;
+  if (d_gamma && !d_stats) return MTFM_ERR_INVALID_ARG;
+  if (!aligned16(d_a) || !aligned16(d_u) || (d_gamma && (!aligned16(d_gamma) || !aligned16(d_beta))) ||
+      (d_stats && (reinterpret_cast<uintptr_t>(d_stats) & 7u)) || (reinterpret_cast<uintptr_t>(d_out) & 3u) ||
+      (reinterpret_cast<uintptr_t>(d_scale) & 3u))
+    return MTFM_ERR_INVALID_ARG;
+  const int groups = (r.D + kGroup - 1) / kGroup;
+  if (rows > 1 && (ld_out < r.D || ld_out % 4 != 0 || ld_scale < groups)) return MTFM_ERR_INVALID_ARG;
+  const MetaLayout L = meta_layout(r.B, r.total_tokens, r.total_t);
+  const MetaView m = meta_view(const_cast<void*>(d_meta), L);
+  return cuda_status(launch_gate_fwd_fp8(m, is_target != 0, rows, r.D, r.eps, d_a,
+                                         reinterpret_cast<const __nv_bfloat16*>(d_u), d_gamma, d_beta,
+                                         Fp8Out{d_out, ld_out, d_scale, ld_scale}, d_stats,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+size_t mtfm_fp8_stack_workspace_bytes(const mtfm_cfg* cfg, int32_t d_model) {
+  Resolved r;
+  if (resolve(cfg, &r) != MTFM_OK || check_stack_cfg(r, d_model) != MTFM_OK) return 0;
+  return fp8_stack_ws(r, d_model).total;
+}
+
+mtfm_status mtfm_fp8_layer_fwd(const mtfm_cfg* cfg, const void* d_meta, int32_t d_model, int is_target,
+                               const mtfm_fp8_layer_weights* weights, float* d_x, void* d_ws, size_t ws_bytes,
+                               void* stream) {
+  const char kind = is_target ? 'T' : 'F';
+  return fp8_stack_fwd(cfg, d_meta, d_model, 1, &kind, weights, d_x, d_ws, ws_bytes, stream);
+}
+
+mtfm_status mtfm_fp8_stack_fwd(const mtfm_cfg* cfg, const void* d_meta, int32_t d_model, int32_t n_layers,
+                               const char* kinds, const mtfm_fp8_layer_weights* layers, float* d_x, void* d_ws,
+                               size_t ws_bytes, void* stream) {
+  return fp8_stack_fwd(cfg, d_meta, d_model, n_layers, kinds, layers, d_x, d_ws, ws_bytes, stream);
 }
 
 size_t mtfm_v2_workspace_bytes(const mtfm_cfg* cfg, int32_t d_model, int32_t d_ff) {

@@ -1,0 +1,185 @@
+// The 8-bit form shared by the producers (norm, gate, quantiser) and the block-scaled
+// product: e4m3 values (4 exponent, 3 mantissa bits, largest 448) with one fp32 scale for
+// each group.  A group is 128 consecutive columns of one row, or a block of 128 x 128; the
+// last ones are ragged.  With m = max(max |v|, 2^-100) over the group
+//     scale = m / 448,   q = e4m3(v * (448 / m))   (round to nearest even, saturating),
+// so that v ~ scale * q with an error of at most half a step of e4m3 (2^-4 relative) for
+// |v| >= m * 2^-6 / 448 and of m * 2^-10 / 448 below that.  The floor keeps 448 / m finite
+// for a group of zeros (q = 0).  A NaN does not enter m; it stays a NaN of its own element.
+// An infinity makes the scale infinite, and the whole group reads back as NaN.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "mtfm_internal.cuh"
+
+namespace mtfm {
+
+constexpr int kGroup = 128;
+constexpr float kE4m3Max = 448.f;
+constexpr float kAmaxFloor = 0x1p-100f;
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// max |x| over the warp (NaN operands are passed over), on every lane.
+__device__ __forceinline__ float warp_absmax(float x) {
+  float y;
+  asm("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float absmax4(const float (&v)[4]) {
+  return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+}
+__device__ __forceinline__ float warp_sum32(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Four columns of a 128-column group per lane.  VEC: columns 4 lane .. 4 lane + 3, read and
+// written as one vector (rows then start on a 4-element boundary); otherwise columns lane,
+// lane + 32, lane + 64, lane + 96, which keeps element-wise accesses coalesced for rows at
+// any offset.  `n` columns of the group exist.
+template <bool VEC>
+__device__ __forceinline__ int lane_col(int lane, int j) {
+  return VEC ? 4 * lane + j : lane + 32 * j;
+}
+template <bool VEC>
+__device__ __forceinline__ void load4(const float* p, int lane, int n, float (&v)[4]) {
+  if (VEC && 4 * lane + 4 <= n) {
+    const float4 t = *reinterpret_cast<const float4*>(p + 4 * lane);
+    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = lane_col<VEC>(lane, j) < n ? p[lane_col<VEC>(lane, j)] : 0.f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, int lane, int n, float (&v)[4]) {
+  if (VEC && 4 * lane + 4 <= n) {
+    const uint2 t = *reinterpret_cast<const uint2*>(p + 4 * lane);
+    v[0] = __uint_as_float(t.x << 16);
+    v[1] = __uint_as_float(t.x & 0xffff0000u);
+    v[2] = __uint_as_float(t.y << 16);
+    v[3] = __uint_as_float(t.y & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = lane_col<VEC>(lane, j) < n ? __bfloat162float(p[lane_col<VEC>(lane, j)]) : 0.f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void put4(float* p, int lane, int n, const float (&v)[4]) {
+  if (VEC && 4 * lane + 4 <= n) {
+    *reinterpret_cast<float4*>(p + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane_col<VEC>(lane, j) < n) p[lane_col<VEC>(lane, j)] = v[j];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void put4(__nv_bfloat16* p, int lane, int n, const float (&v)[4]) {
+  if (VEC && 4 * lane + 4 <= n) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+    uint2 t;
+    t.x = *reinterpret_cast<uint32_t*>(&lo);
+    t.y = *reinterpret_cast<uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(p + 4 * lane) = t;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane_col<VEC>(lane, j) < n) p[lane_col<VEC>(lane, j)] = __float2bfloat16_rn(v[j]);
+  }
+}
+// q = e4m3(v * inv)
+template <bool VEC>
+__device__ __forceinline__ void put4_e4m3(uint8_t* p, int lane, int n, const float (&v)[4], float inv) {
+  const uint32_t t = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+  if (VEC && 4 * lane + 4 <= n) {
+    *reinterpret_cast<uint32_t*>(p + 4 * lane) = t;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane_col<VEC>(lane, j) < n) p[lane_col<VEC>(lane, j)] = (uint8_t)(t >> (8 * j));
+  }
+}
+
+// Quantises the warp's 128-column group (4 columns a lane) and writes it with its scale.
+// Columns past n must hold zeros.
+template <bool VEC>
+__device__ __forceinline__ void quant_group(const float (&v)[4], int lane, int n, uint8_t* q, float* scale) {
+  const float m = fmaxf(warp_absmax(absmax4(v)), kAmaxFloor);
+  put4_e4m3<VEC>(q, lane, n, v, kE4m3Max / m);
+  if (lane == 0) *scale = m / kE4m3Max;
+}
+
+// Matrices of the 8-bit entry points.  ld: row pitch in elements.
+struct MatIn {
+  const void* p;
+  int64_t ld;
+  int type;  // mtfm_dtype
+};
+struct MatOut {
+  void* p;
+  int64_t ld;
+  int type;
+};
+struct Fp8Out {
+  uint8_t* q;
+  int64_t ld;
+  float* scale;
+  int64_t ld_scale;
+};
+struct Fp8In {
+  const uint8_t* q;
+  int64_t ld;
+  const float* scale;
+  int64_t ld_scale;
+};
+
+constexpr int kMaxNormDim = 16384;
+
+// A row starts on a boundary of 4 elements of `size` bytes, for every row.
+inline bool rows_vec4(const void* p, int64_t ld, int size) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(4 * size - 1)) == 0 && ld % 4 == 0;
+}
+inline int dtype_size(int type) { return type == MTFM_BF16 ? 2 : 4; }
+
+// err (may be NULL): a device error word; the kernel does nothing while it is not zero.
+// row_map (may be NULL): row i reads row row_map[i] of x; delta and x_out must then be NULL.
+cudaError_t launch_add_rmsnorm_fp8(const int32_t* err, int rows, int dim, const MatIn& x, const MatIn& delta,
+                                   const int32_t* row_map, const float* w, float eps, const MatOut& x_out,
+                                   const Fp8Out& out, float* rstd, cudaStream_t st);
+// Blocks of the backward's row pass: each writes one partial row of dw.
+constexpr int kNormBwdBlocks = 592;
+cudaError_t launch_rmsnorm_bwd(int rows, int dim, const MatIn& x, const float* w, const float* rstd, const MatIn& dy,
+                               const MatIn& dres, const MatOut& dx, float* dw, float* partials, cudaStream_t st);
+cudaError_t launch_gate_fwd_fp8(const MetaView& m, bool target, int rows, int D, float eps, const float* a,
+                                const __nv_bfloat16* u, const float* gamma, const float* beta, const Fp8Out& out,
+                                float* stats, cudaStream_t st);
+cudaError_t launch_fp8_quant(int rows, int cols, const MatIn& x, int block_rows, const Fp8Out& out, cudaStream_t st);
+
+// Epilogue of the block-scaled product: out = act(C) + res, written into up to four column
+// segments (each its own matrix, borders at multiples of 32) and, with a row map, into row
+// row_map[i] of out and res for output row i.
+struct Fp8Epi {
+  int act;       // mtfm_act
+  int out_type;  // mtfm_dtype of the segments and of res
+  int n_seg;
+  int seg_begin[5];
+  void* seg_ptr[4];
+  int64_t seg_ld[4];
+  const void* res;  // NULL: none (one segment only)
+  int64_t ld_res;
+  const int32_t* row_map;
+};
+cudaError_t launch_gemm_fp8(int32_t* err, int M, int N, int K, const Fp8In& a, const Fp8In& b, const Fp8Epi& epi,
+                            cudaStream_t st);
+
+}  // namespace mtfm

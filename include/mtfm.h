@@ -405,6 +405,112 @@ mtfm_status mtfm_v2_target_layer_fwd(const mtfm_cfg* cfg, const void* d_meta, in
                                      size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * 8-bit projections (no counterpart on the pages, which serve in bf16 with 2:4
+ * sparse projections; an e4m3 operand doubles the tensor rate without pruning).
+ * An 8-bit matrix is e4m3 values (4 exponent, 3 mantissa bits, largest 448; one
+ * byte each) with one fp32 scale per group: 128 consecutive columns of one row
+ * (activations: scale [rows, ceil(cols / 128)]) or a block of 128 x 128
+ * (weights: scale [ceil(rows / 128), ceil(cols / 128)]); the last groups are
+ * ragged.  With m = max(max |v|, 2^-100) over the group
+ *     scale = m / 448,   q = e4m3(v * (448 / m))   (nearest even, saturating)
+ * and v ~ scale * q.  A NaN stays a NaN of its own element and does not enter m;
+ * an infinity makes its group's scale infinite (the group reads back as NaN).
+ *
+ * In the calls below a matrix is a device pointer, its type (mtfm_dtype) where it
+ * is not fixed, and its row pitch `ld*` in elements (>= its columns; scales too).
+ * Columns between a row's end and its pitch are neither read nor written.  Pitches
+ * and bases need the alignment of one element only, unless stated; rows that start
+ * on 4-element boundaries (16 bytes for the product's output) take vector accesses.
+ * Zero rows launch nothing (mtfm_rmsnorm_bwd still zeroes dw).  Sums and statistics
+ * are fp32; results do not depend on timing (no atomics).
+ * ------------------------------------------------------------------------- */
+typedef enum { MTFM_F32 = 0, MTFM_BF16 = 1 } mtfm_dtype;
+typedef enum { MTFM_ACT_NONE = 0, MTFM_ACT_SILU = 1 } mtfm_act;
+
+/* Residual addition, RMSNorm and quantisation in one pass:
+ *   h = x + delta,  rstd = 1 / sqrt(mean(h^2) + eps),  (out, scale) = groups of h rstd w,
+ *   x_out = h rounded to x's type (the norm takes h before that rounding).
+ * x, x_out [rows, dim] (x_type); delta [rows, dim] or NULL (then x_out must be NULL);
+ * x_out may be x itself, or NULL (the sum is not kept).  w fp32 [dim]; eps <= 0 selects
+ * 1e-6; out [rows, dim]; scale [rows, ceil(dim / 128)]; rstd fp32 [rows] or NULL (what
+ * the backward needs).  dim in [1, 16384]. */
+mtfm_status mtfm_add_rmsnorm_fp8(int32_t rows, int32_t dim, const void* d_x, int32_t x_type, int64_t ldx,
+                                 const void* d_delta, int32_t delta_type, int64_t ld_delta, const float* d_w,
+                                 float eps, void* d_x_out, int64_t ld_x_out, uint8_t* d_out, int64_t ld_out,
+                                 float* d_scale, int64_t ld_scale, float* d_rstd, void* stream);
+
+/* Backward of the norm (the quantisation passes gradients through unchanged):
+ *   g = dy w,  dx = rstd (g - x rstd^2 mean(g x)) + dres,  dw = sum over rows of dy x rstd.
+ * x: the stream the forward normalised (its x_out, or x where delta was NULL); dx is the
+ * gradient of it, and so of both x and delta.  dres: gradient arriving along the residual
+ * stream, or NULL.  dy, dres: their own types; dx: x's type, and may be dy or dres where
+ * type and pitch agree.  dw fp32 [dim], overwritten.  d_ws: at least
+ * mtfm_rmsnorm_bwd_workspace_bytes(rows, dim) bytes, 16-byte aligned, not shared by calls
+ * that may overlap (0 for an unsupported dim).  dim in [1, 16384]. */
+size_t mtfm_rmsnorm_bwd_workspace_bytes(int32_t rows, int32_t dim);
+mtfm_status mtfm_rmsnorm_bwd(int32_t rows, int32_t dim, const void* d_x, int32_t x_type, int64_t ldx,
+                             const float* d_w, const float* d_rstd, const void* d_dy, int32_t dy_type,
+                             int64_t ld_dy, const void* d_dres, int32_t dres_type, int64_t ld_dres, void* d_dx,
+                             int64_t ld_dx, float* d_dw, void* d_ws, size_t ws_bytes, void* stream);
+
+/* The gate of mtfm_gate_fwd with its output in 8 bits: (out, scale) = groups of
+ * GLN(A) (*) U (A (*) U when d_gamma is NULL).  out [rows, hq*head_dim], 4-byte aligned
+ * with a pitch that is a multiple of 4; everything else as mtfm_gate_fwd. */
+mtfm_status mtfm_gate_fwd_fp8(const mtfm_cfg* cfg, const void* d_meta, int is_target, const float* d_a,
+                              const uint16_t* d_u, const float* d_gamma, const float* d_beta, uint8_t* d_out,
+                              int64_t ld_out, float* d_scale, int64_t ld_scale, float* d_stats, void* stream);
+
+/* Quantises x [rows, cols] (fp32 or bf16) with one scale per 1 x 128 group (block_rows = 1)
+ * or per 128 x 128 block (block_rows = 128). */
+mtfm_status mtfm_fp8_quant(int32_t rows, int32_t cols, const void* d_x, int32_t x_type, int64_t ldx,
+                           int32_t block_rows, uint8_t* d_out, int64_t ld_out, float* d_scale, int64_t ld_scale,
+                           void* stream);
+
+/* Block-scaled product: out[m, n] = act(sum_k A[m, k] B[n, k]) + res[m, n], with A [m, k] in
+ * 1 x 128 groups and B [n, k] in 128 x 128 blocks (a weight, "out x in"; the gradient
+ * dX = dY W is the same call on quantised dY and on the quantised transpose of W).
+ * Products of one 128-deep block are summed by the tensor cores, scaled, and added in fp32.
+ * A and B: 16-byte aligned, pitches multiples of 16 (a single row may have any pitch).
+ * out, res: out_type; res may be NULL, or out itself.  k >= 1.
+ * d_status: device word, zeroed once by the caller; a call on a word that is not zero does
+ * nothing, and a device wait that gives up sets it.  mtfm_fp8_check synchronises `stream`
+ * and returns what it says (MTFM_OK, MTFM_ERR_TIMEOUT, MTFM_ERR_BOUNDS). */
+mtfm_status mtfm_fp8_gemm(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, int64_t lda, const float* d_a_scale,
+                          int64_t ld_a_scale, const uint8_t* d_b, int64_t ldb, const float* d_b_scale,
+                          int64_t ld_b_scale, int32_t act, const void* d_res, int64_t ld_res, void* d_out,
+                          int32_t out_type, int64_t ld_out, int32_t* d_status, void* stream);
+mtfm_status mtfm_fp8_check(const int32_t* d_status, void* stream);
+
+/* The backbone layers of mtfm_layer_fwd / mtfm_stack_fwd with 8-bit projections: X~ leaves
+ * the RMSNorm, and Y the gate, as e4m3 in 1 x 128 groups; w_in, w_kv and w_o are e4m3 in
+ * 128 x 128 blocks (mtfm_fp8_quant with block_rows = 128), of the shapes of
+ * mtfm_layer_weights, pitches multiples of 16.  Attention runs on bf16 U, Q, K, V as there;
+ * X and its residual additions stay fp32.  Same arguments, shapes, checks and errors
+ * otherwise; d_ws of at least mtfm_fp8_stack_workspace_bytes(cfg, d_model) bytes. */
+typedef struct mtfm_fp8_weight {
+  const uint8_t* data; /* NULL: absent (w_kv of a Full layer) */
+  int64_t ld;
+  const float* scale;
+  int64_t ld_scale;
+} mtfm_fp8_weight;
+typedef struct mtfm_fp8_layer_weights {
+  const float* rms_w;
+  mtfm_fp8_weight w_in;
+  mtfm_fp8_weight w_kv;
+  mtfm_fp8_weight w_o;
+  const float* gamma;
+  const float* beta;
+} mtfm_fp8_layer_weights;
+
+size_t mtfm_fp8_stack_workspace_bytes(const mtfm_cfg* cfg, int32_t d_model);
+mtfm_status mtfm_fp8_layer_fwd(const mtfm_cfg* cfg, const void* d_meta, int32_t d_model, int is_target,
+                               const mtfm_fp8_layer_weights* weights, float* d_x, void* d_ws, size_t ws_bytes,
+                               void* stream);
+mtfm_status mtfm_fp8_stack_fwd(const mtfm_cfg* cfg, const void* d_meta, int32_t d_model, int32_t n_layers,
+                               const char* kinds, const mtfm_fp8_layer_weights* layers, float* d_x, void* d_ws,
+                               size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Self-test of failure detection (no counterpart on the pages).  Launches one
  * CTA that waits, with the bounded mbarrier wait every tensor-core kernel of
  * this library uses, on a barrier nothing arrives on; after limit_cycles SM
