@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "mtfm_internal.cuh"
+#include "tma_host.cuh"
 
 namespace mtfm {
 
@@ -41,82 +42,115 @@ __device__ __forceinline__ float warp_sum32(float x) {
   return x;
 }
 
-// Four columns of a 128-column group per lane.  VEC: columns 4 lane .. 4 lane + 3, read and
-// written as one vector (rows then start on a 4-element boundary); otherwise columns lane,
-// lane + 32, lane + 64, lane + 96, which keeps element-wise accesses coalesced for rows at
-// any offset.  `n` columns of the group exist.
+// 1 / x to one unit in the last place, subnormal results included.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four columns of a 128-column group per lane, of which the group's row has n.
+// VEC (rows of a multiple of 4 columns that start on 4-element boundaries): columns 4 lane ..
+// 4 lane + 3 as one vector.  Otherwise columns lane, lane + 32, lane + 64, lane + 96, which
+// keeps element-wise accesses coalesced for rows at any offset.
+template <typename T>
+struct Raw;  // four elements as they are in memory
+template <>
+struct Raw<float> { float4 v; };
+template <>
+struct Raw<__nv_bfloat16> { uint2 v; };
+
 template <bool VEC>
-__device__ __forceinline__ int lane_col(int lane, int j) {
-  return VEC ? 4 * lane + j : lane + 32 * j;
+__device__ __forceinline__ bool lane_has(int lane, int j, int n) { return (VEC ? 4 * lane : lane + 32 * j) < n; }
+template <bool VEC>
+__device__ __forceinline__ int lane_col(int lane, int j) { return VEC ? 4 * lane + j : lane + 32 * j; }
+
+template <bool VEC>
+__device__ __forceinline__ Raw<float> load_raw(const float* p, int lane, int n) {
+  Raw<float> r{make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (VEC) {
+    if (4 * lane < n) r.v = *reinterpret_cast<const float4*>(p + 4 * lane);
+  } else {
+    if (lane < n) r.v.x = p[lane];
+    if (lane + 32 < n) r.v.y = p[lane + 32];
+    if (lane + 64 < n) r.v.z = p[lane + 64];
+    if (lane + 96 < n) r.v.w = p[lane + 96];
+  }
+  return r;
 }
 template <bool VEC>
-__device__ __forceinline__ void load4(const float* p, int lane, int n, float (&v)[4]) {
-  if (VEC && 4 * lane + 4 <= n) {
-    const float4 t = *reinterpret_cast<const float4*>(p + 4 * lane);
-    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+__device__ __forceinline__ Raw<__nv_bfloat16> load_raw(const __nv_bfloat16* p, int lane, int n) {
+  Raw<__nv_bfloat16> r{make_uint2(0, 0)};
+  if (VEC) {
+    if (4 * lane < n) r.v = *reinterpret_cast<const uint2*>(p + 4 * lane);
   } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    uint32_t t[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = lane_col<VEC>(lane, j) < n ? p[lane_col<VEC>(lane, j)] : 0.f;
+    for (int j = 0; j < 4; ++j) t[j] = lane + 32 * j < n ? h[lane + 32 * j] : 0;
+    r.v = make_uint2(t[0] | (t[1] << 16), t[2] | (t[3] << 16));
   }
+  return r;
 }
-template <bool VEC>
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, int lane, int n, float (&v)[4]) {
-  if (VEC && 4 * lane + 4 <= n) {
-    const uint2 t = *reinterpret_cast<const uint2*>(p + 4 * lane);
-    v[0] = __uint_as_float(t.x << 16);
-    v[1] = __uint_as_float(t.x & 0xffff0000u);
-    v[2] = __uint_as_float(t.y << 16);
-    v[3] = __uint_as_float(t.y & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = lane_col<VEC>(lane, j) < n ? __bfloat162float(p[lane_col<VEC>(lane, j)]) : 0.f;
-  }
+__device__ __forceinline__ void unpack(const Raw<float>& r, float (&v)[4]) {
+  v[0] = r.v.x; v[1] = r.v.y; v[2] = r.v.z; v[3] = r.v.w;
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, float (&v)[4]) {
+  v[0] = __uint_as_float(r.v.x << 16);
+  v[1] = __uint_as_float(r.v.x & 0xffff0000u);
+  v[2] = __uint_as_float(r.v.y << 16);
+  v[3] = __uint_as_float(r.v.y & 0xffff0000u);
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void load4(const T* p, int lane, int n, float (&v)[4]) {
+  unpack(load_raw<VEC>(p, lane, n), v);
 }
 template <bool VEC>
 __device__ __forceinline__ void put4(float* p, int lane, int n, const float (&v)[4]) {
-  if (VEC && 4 * lane + 4 <= n) {
-    *reinterpret_cast<float4*>(p + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+  if (VEC) {
+    if (4 * lane < n) *reinterpret_cast<float4*>(p + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (lane_col<VEC>(lane, j) < n) p[lane_col<VEC>(lane, j)] = v[j];
+      if (lane + 32 * j < n) p[lane + 32 * j] = v[j];
   }
 }
 template <bool VEC>
 __device__ __forceinline__ void put4(__nv_bfloat16* p, int lane, int n, const float (&v)[4]) {
-  if (VEC && 4 * lane + 4 <= n) {
+  if (VEC) {
     __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
     uint2 t;
     t.x = *reinterpret_cast<uint32_t*>(&lo);
     t.y = *reinterpret_cast<uint32_t*>(&hi);
-    *reinterpret_cast<uint2*>(p + 4 * lane) = t;
+    if (4 * lane < n) *reinterpret_cast<uint2*>(p + 4 * lane) = t;
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (lane_col<VEC>(lane, j) < n) p[lane_col<VEC>(lane, j)] = __float2bfloat16_rn(v[j]);
+      if (lane + 32 * j < n) p[lane + 32 * j] = __float2bfloat16_rn(v[j]);
   }
 }
 // q = e4m3(v * inv)
 template <bool VEC>
 __device__ __forceinline__ void put4_e4m3(uint8_t* p, int lane, int n, const float (&v)[4], float inv) {
   const uint32_t t = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-  if (VEC && 4 * lane + 4 <= n) {
-    *reinterpret_cast<uint32_t*>(p + 4 * lane) = t;
+  if (VEC) {
+    if (4 * lane < n) *reinterpret_cast<uint32_t*>(p + 4 * lane) = t;
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (lane_col<VEC>(lane, j) < n) p[lane_col<VEC>(lane, j)] = (uint8_t)(t >> (8 * j));
+      if (lane + 32 * j < n) p[lane + 32 * j] = (uint8_t)(t >> (8 * j));
   }
 }
 
-// Quantises the warp's 128-column group (4 columns a lane) and writes it with its scale.
-// Columns past n must hold zeros.
+// Quantises the warp's 128-column group (columns past n hold zeros), writes its bytes and
+// returns m = max(max |v|, 2^-100), from which the caller writes the scale m / 448.  448 / m is
+// 448 times an approximate reciprocal: 3 half steps of fp32 from the quotient, far below half a
+// step of e4m3, for a fifth of a division's instructions (of which a group would need 32 lanes').
 template <bool VEC>
-__device__ __forceinline__ void quant_group(const float (&v)[4], int lane, int n, uint8_t* q, float* scale) {
+__device__ __forceinline__ float quant_group(const float (&v)[4], int lane, int n, uint8_t* q) {
   const float m = fmaxf(warp_absmax(absmax4(v)), kAmaxFloor);
-  put4_e4m3<VEC>(q, lane, n, v, kE4m3Max / m);
-  if (lane == 0) *scale = m / kE4m3Max;
+  put4_e4m3<VEC>(q, lane, n, v, kE4m3Max * rcp_approx(m));
+  return m;
 }
 
 // Matrices of the 8-bit entry points.  ld: row pitch in elements.
@@ -145,7 +179,7 @@ struct Fp8In {
 
 constexpr int kMaxNormDim = 16384;
 
-// A row starts on a boundary of 4 elements of `size` bytes, for every row.
+// Every row starts on a boundary of 4 elements of `size` bytes.
 inline bool rows_vec4(const void* p, int64_t ld, int size) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(4 * size - 1)) == 0 && ld % 4 == 0;
 }

@@ -1,0 +1,242 @@
+// Backward of the RMSNorm.  With g = dy w and x the stream that was normalised:
+//   dx = r (g - x r^2 mean_j(g_j x_j)) + dres,      dw_j = sum_rows dy_j x_j r
+//
+// One pass over x, dy and dres (bound by memory).  Blocks stride over the rows; a lane keeps
+// the same columns for all of its rows, so dw is summed in registers, in an order that depends
+// on the sizes alone, and leaves a block as one partial row; a second kernel adds those up.
+#include <algorithm>
+#include <type_traits>
+
+#include "fp8.cuh"
+
+namespace mtfm {
+namespace {
+
+struct None {};  // no dres
+
+template <typename XT, typename YT, typename RT>
+struct BwdArgs {
+  int rows, dim, W;
+  const XT* x;
+  int64_t ldx;
+  const float* w;
+  const float* rstd;
+  const YT* dy;
+  int64_t ld_dy;
+  const RT* dres;
+  int64_t ld_dres;
+  XT* dx;
+  int64_t ld_dx;
+  float* partials;
+};
+
+// C groups a warp: 4 with the next row's loads in flight (blocks of 8 warps, rows of up to
+// 4096 columns), 8 without (16 warps, 16384 columns; 128 registers do not hold a second row).
+template <int C>
+constexpr int kThreadsB = C == 8 ? 512 : 256;
+
+template <typename XT, typename YT, typename RT, int C, bool VEC>
+__global__ void __launch_bounds__(kThreadsB<C>, C == 8 ? 1 : 2)
+rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
+  constexpr bool kRes = !std::is_same<RT, None>::value;
+  constexpr bool kAhead = C < 8;
+  constexpr int kWarps = kThreadsB<C> / 32;
+  using RRaw = typename std::conditional<kRes, RT, XT>::type;
+  extern __shared__ float s_dw[];  // [rows of a block - 1][dim]
+  __shared__ float s_part[2][kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int W = p.W, sub = warp % W, slot = warp / W, R = kWarps / W;
+  const int G = (p.dim + kGroup - 1) / kGroup;
+  pdl_wait();
+  pdl_trigger();
+  float dw[C][4];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[i][j] = 0.f;
+  Raw<XT> xr[C];
+  Raw<YT> yr[C];
+  Raw<RRaw> rr[C];
+  float r_next = 0.f;
+  auto load_row = [&](int64_t row) {
+    if (row >= p.rows) return;
+    r_next = p.rstd[row];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int g = i * W + sub;
+      if (g < G) {
+        xr[i] = load_raw<VEC>(p.x + row * p.ldx + g * kGroup, lane, p.dim - g * kGroup);
+        yr[i] = load_raw<VEC>(p.dy + row * p.ld_dy + g * kGroup, lane, p.dim - g * kGroup);
+        if constexpr (kRes && kAhead) rr[i] = load_raw<VEC>(p.dres + row * p.ld_dres + g * kGroup, lane, p.dim - g * kGroup);
+      }
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t row = (int64_t)blockIdx.x * R + slot;
+  if (kAhead) load_row(row);
+  int flip = 0;
+  // every warp of the block makes the same number of rounds (the barrier below)
+  for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < p.rows; row0 += step, row += step, flip ^= 1) {
+    const bool live = row < p.rows;
+    if (!kAhead) load_row(row);
+    const float r = r_next;
+    float xv[C][4], gv[C][4];
+    Raw<RRaw> res[C];
+    float s = 0.f;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int g = i * W + sub;
+        if (g < G) {
+          unpack(xr[i], xv[i]);
+          unpack(yr[i], gv[i]);
+          res[i] = rr[i];
+          float ww[4];
+          load4<VEC>(p.w + g * kGroup, lane, p.dim - g * kGroup, ww);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            dw[i][j] = fmaf(gv[i][j], xv[i][j] * r, dw[i][j]);
+            gv[i][j] *= ww[j];
+            s = fmaf(gv[i][j], xv[i][j], s);
+          }
+        }
+      }
+    }
+    if (kAhead) load_row(row + step);
+    s = warp_sum32(s);
+    if (W > 1) {
+      if (lane == 0) s_part[flip][warp] = s;
+      __syncthreads();
+      s = 0.f;
+      for (int k = 0; k < W; ++k) s += s_part[flip][warp - sub + k];
+    }
+    if (live) {
+      const float c = s / (float)p.dim * r * r;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int g = i * W + sub;
+        if (g < G) {
+          const int n = p.dim - g * kGroup;
+          float o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = r * fmaf(-xv[i][j], c, gv[i][j]);
+          if constexpr (kRes) {
+            float t[4];
+            if constexpr (kAhead) unpack(res[i], t);
+            else load4<VEC>(p.dres + row * p.ld_dres + g * kGroup, lane, n, t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] += t[j];
+          }
+          put4<VEC>(p.dx + row * p.ld_dx + g * kGroup, lane, n, o);
+        }
+      }
+    }
+  }
+  // the block's partial row: slots 1.. hand theirs over through shared memory
+  if (R > 1) {
+    if (slot > 0)
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int g = i * W + sub;
+        if (g < G)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int c = g * kGroup + lane_col<VEC>(lane, j);
+            if (c < p.dim) s_dw[(size_t)(slot - 1) * p.dim + c] = dw[i][j];
+          }
+      }
+    __syncthreads();
+  }
+  if (slot == 0)
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int g = i * W + sub;
+      if (g < G)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = g * kGroup + lane_col<VEC>(lane, j);
+          if (c < p.dim) {
+            float t = dw[i][j];
+            for (int k = 0; k < R - 1; ++k) t += s_dw[(size_t)k * p.dim + c];
+            p.partials[(size_t)blockIdx.x * p.dim + c] = t;
+          }
+        }
+    }
+}
+
+// dw = sum of the partial rows: 8 columns (one 32-byte sector) a block, 32 threads down each,
+// fixed order.
+__global__ void __launch_bounds__(256)
+dw_reduce_kernel(const float* __restrict__ partials, int n_part, int dim, float* __restrict__ dw) {
+  __shared__ float s[8][33];
+  pdl_wait();
+  pdl_trigger();
+  const int cx = threadIdx.x & 7, ry = threadIdx.x >> 3;
+  const int c = blockIdx.x * 8 + cx;
+  float t = 0.f;
+  if (c < dim) {
+#pragma unroll 8
+    for (int b = ry; b < n_part; b += 32) t += partials[(size_t)b * dim + c];
+  }
+  s[cx][ry] = t;
+  __syncthreads();
+  t = warp_sum32(s[threadIdx.x >> 5][threadIdx.x & 31]);
+  const int co = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if ((threadIdx.x & 31) == 0 && co < dim) dw[co] = t;
+}
+
+inline int pow2_ceil(int v) {
+  int p = 1;
+  while (p < v) p *= 2;
+  return p;
+}
+
+template <typename XT, typename YT, typename RT, int C, bool VEC>
+cudaError_t go(BwdArgs<XT, YT, RT>& a, float* dw, cudaStream_t st) {
+  constexpr int warps = kThreadsB<C> / 32;
+  const int G = (a.dim + kGroup - 1) / kGroup;
+  a.W = pow2_ceil((G + C - 1) / C);
+  const int R = warps / a.W;
+  const size_t smem = sizeof(float) * (size_t)(R - 1) * a.dim;  // R W C 128 columns at most: under 33 KB
+  const int per_sm = C == 8 ? 1 : 2;  // the kernel's launch bound
+  const int blocks = (int)std::min<int64_t>(std::min(kNormBwdBlocks, per_sm * sm_count()), ((int64_t)a.rows + R - 1) / R);
+  cudaError_t e = launch_pdl(rmsnorm_bwd_kernel<XT, YT, RT, C, VEC>, dim3(blocks), dim3(32 * warps), smem, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(dw_reduce_kernel, dim3((a.dim + 7) / 8), dim3(256), 0, st, (const float*)a.partials, blocks, a.dim, dw);
+}
+
+template <typename XT, typename YT, typename RT>
+cudaError_t types(int rows, int dim, const MatIn& x, const float* w, const float* rstd, const MatIn& dy, const MatIn& dres,
+                  const MatOut& dx, float* dw, float* partials, cudaStream_t st) {
+  BwdArgs<XT, YT, RT> a{rows, dim, 1, static_cast<const XT*>(x.p), x.ld, w, rstd, static_cast<const YT*>(dy.p), dy.ld,
+                        static_cast<const RT*>(dres.p), dres.ld, static_cast<XT*>(dx.p), dx.ld, partials};
+  const bool vec = dim % 4 == 0 && rows_vec4(x.p, x.ld, sizeof(XT)) && rows_vec4(dy.p, dy.ld, sizeof(YT)) &&
+                   rows_vec4(w, 4, 4) && (!dres.p || rows_vec4(dres.p, dres.ld, dtype_size(dres.type))) &&
+                   rows_vec4(dx.p, dx.ld, sizeof(XT));
+  if (dim <= 32 * kGroup)
+    return vec ? go<XT, YT, RT, 4, true>(a, dw, st) : go<XT, YT, RT, 4, false>(a, dw, st);
+  return vec ? go<XT, YT, RT, 8, true>(a, dw, st) : go<XT, YT, RT, 8, false>(a, dw, st);
+}
+
+template <typename XT, typename YT, typename... Args>
+cudaError_t with_res(const MatIn& dres, Args&&... args) {
+  if (!dres.p) return types<XT, YT, None>(args...);
+  if (dres.type == MTFM_BF16) return types<XT, YT, __nv_bfloat16>(args...);
+  return types<XT, YT, float>(args...);
+}
+template <typename XT, typename... Args>
+cudaError_t with_dy(const MatIn& dy, const MatIn& dres, Args&&... args) {
+  if (dy.type == MTFM_BF16) return with_res<XT, __nv_bfloat16>(dres, args...);
+  return with_res<XT, float>(dres, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_bwd(int rows, int dim, const MatIn& x, const float* w, const float* rstd, const MatIn& dy,
+                               const MatIn& dres, const MatOut& dx, float* dw, float* partials, cudaStream_t st) {
+  if (rows <= 0) return cudaMemsetAsync(dw, 0, sizeof(float) * (size_t)dim, st);
+  if (x.type == MTFM_BF16) return with_dy<__nv_bfloat16>(dy, dres, rows, dim, x, w, rstd, dy, dres, dx, dw, partials, st);
+  return with_dy<float>(dy, dres, rows, dim, x, w, rstd, dy, dres, dx, dw, partials, st);
+}
+
+}  // namespace mtfm
