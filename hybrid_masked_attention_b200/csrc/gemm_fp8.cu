@@ -1,19 +1,33 @@
 // Block-scaled product of two e4m3 matrices (fp8.cuh):
 //   C[i, j] = sum_b sa[i, b] sb[j / 128, b] sum_{k in block b} qa[i, k] qb[j, k],   b = k / 128
 //   out = act(C) + res
-// TMA brings 128-byte K blocks of A and B (128-byte swizzle, both K-major) into a ring;
-// tcgen05 MMAs (kind::f8f6f4) form the partial product of one 128-deep block in TMEM, and
-// the epilogue warps add it, times its scale, to fp32 sums in registers.  A block's scale is
-// one factor per row of the tile (the tile's columns of one weight block share sb), so the
-// whole scaling costs one FMA an element and block.  TMEM holds 2 to 4 partial products: the
-// MMAs of the next block run while the last one is read.
 //
-// Persistent CTAs (one per SM) stride over 128 x BN tiles.  Warp 0 issues TMA, warp 1 the
-// MMAs; warps 4..11 are two warpgroups, each on half of the tile's columns, one TMEM lane
-// (row) a thread.  The sums take BN / 2 registers a thread; for BN = 256 the registers of
-// the first four warps are handed over (setmaxnreg).  Every wait is bounded; a wait that
-// gives up raises the CTA's abort flag, the roles drain what they issued, and the error
-// word gets the timeout bit.
+// Pairs of CTAs (a cluster of 2, one SM each) compute 256 x BN tiles with tcgen05.mma
+// cta_group::2 (kind::f8f6f4): each CTA brings its 128 rows of A and half of the tile's rows
+// of B by TMA (128-byte K blocks, 128-byte swizzle), the MMA reads both CTAs' B, and each CTA's
+// TMEM receives its 128 rows.  Halving the B traffic of a CTA is what the pair is for: at
+// 8192^3 the L2 would have to deliver 8.6 GB to single CTAs with 128 x 128 tiles, and delivers
+// 4.3 GB to pairs with 256 x 256.
+//
+// The MMAs sum one 128-deep block of 128 columns at a time; the epilogue warps add it, times
+// its scale, to fp32 sums in registers: one packed FMA for two elements and block, since a
+// thread has one row (sa) and its columns lie in one weight block (sb).  Four warpgroups of 64
+// columns each: 16 warps hide the latency of reading TMEM (8 warps of 128 columns took 1.2x as
+// long at 8192^3).
+//
+// BN = 256: the tile is two halves, each with its own MMA-issuing warp, two TMEM buffers and
+// two warpgroups, so that one half's block is read while the tensor pipe works on the other's.
+// BN = 128: four TMEM buffers; two warpgroups take the even tiles and two the odd ones.
+//
+// Warp 0 issues TMA; warps 1 and 3 of the leading CTA issue the MMAs of the pair (one warp for
+// both halves kept the tensor pipe waiting: 412 against 311 us at 8192^3 with nothing else in
+// the way); warp 2 brings the A scales, 128 rows a block, to shared memory (read from global
+// memory by the epilogue warps themselves, 32 rows a warp and each row in 4 warpgroups, they
+// cost 100 us of 560); warps 4..19 are the warpgroups, one TMEM lane (row) a thread.  Their 64
+// sums a thread take registers that the first four warps hand over (setmaxnreg).
+// Every wait is bounded; a wait that gives up raises its CTA's abort flag, the other CTA's own
+// waits then run out too, both meet at the cluster barrier, and the error word gets the
+// timeout bit.
 #include <cuda.h>
 
 #include <algorithm>
@@ -29,10 +43,14 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kBM = 128;
+constexpr int kBM = 128;  // rows of a CTA; a pair's tile has 256
 constexpr uint32_t kABytes = kBM * kGroup;
-constexpr int kEpiWarps = 8;
-constexpr int kThreadsG = 128 + 32 * kEpiWarps;
+constexpr int kGroupsWG = 4;  // epilogue warpgroups, 64 columns each
+constexpr int kCols = 64;
+constexpr int kThreadsG = 128 + 128 * kGroupsWG;
+// Registers: 640 threads are launched with 96 (61440); 128 x 32 + 512 x 112 are as many.
+constexpr int kRegsFew = 32, kRegsMany = 112;
+constexpr uint32_t kBoxBytes = 128 * 128;  // a warpgroup's staged box: 128 rows x 128 bytes
 
 struct Args {
   int32_t* err;
@@ -42,73 +60,158 @@ struct Args {
   const float* sb;
   int64_t ld_sb;
   Fp8Epi epi;
-  bool vec;  // every output (and res) row starts on a 16-byte boundary
+  int n_group;  // tiles are walked in bands of n_group tile columns (see launch)
+  bool vec;     // every output (and res) row starts on a 16-byte boundary
 };
 
 template <int BN>
-constexpr uint32_t stage_bytes_g() { return kABytes + (uint32_t)BN * kGroup; }
+constexpr uint32_t stage_bytes_g() { return kABytes + (uint32_t)(BN / 2) * kGroup; }
 template <int BN>
-constexpr int stages_g() { return BN == 256 ? 4 : BN == 128 ? 6 : 8; }
+constexpr int stages_g() { return BN == 256 ? 5 : 6; }
+// Parts of a tile with their own MMAs, and TMEM buffers of a part (512 columns in all).
 template <int BN>
-constexpr int acc_bufs() { return BN == 256 ? 2 : 4; }
+constexpr int parts_g() { return BN / 128; }
 template <int BN>
-constexpr size_t smem_g() { return (size_t)stages_g<BN>() * stage_bytes_g<BN>() + 1024; }
+constexpr int acc_bufs() { return 512 / BN; }
+constexpr int kSlots = 5;  // blocks of A scales in shared memory
+// Dynamic shared memory (there is no static): the ring, the staged boxes, the scales, barriers.
+template <int BN>
+constexpr uint32_t stage_off() { return stages_g<BN>() * stage_bytes_g<BN>(); }
+template <int BN>
+constexpr uint32_t scale_off() { return stage_off<BN>() + kGroupsWG * kBoxBytes; }
+template <int BN>
+constexpr uint32_t bars_off() { return scale_off<BN>() + kSlots * 128 * 4; }
+template <int BN>
+constexpr size_t smem_g() { return bars_off<BN>() + 512; }
+struct Bars {
+  uint64_t full[6], empty[6];           // ring stages
+  uint64_t acc_full[8], acc_empty[4];   // TMEM buffers (acc_full: per part, or per set)
+  uint64_t sc_full[2 * kSlots], sc_empty[kSlots];  // scales (sc_full: per set)
+  uint64_t drain[2];
+  uint32_t tmem, skip;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 512 && smem_g<256>() <= 232448, "shared memory of an SM");
 
 // kind::f8f6f4, e4m3 x e4m3 -> fp32 (formats 0), both operands K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
-                                       uint32_t accumulate) {
+
+// ---------------------------------------------------------------- CTA pairs
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// shared::cluster address of a shared::cta address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// Relaxed: what it hands over is TMEM that this warp has finished reading (tcgen05.wait::ld and
+// the fence before the arrival); no write to memory has to become visible.  (A release at
+// cluster scope is a memory fence: 4096^3 took 182 us with it and 105 without.)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// TMA load into this CTA's shared memory, completion counted on a barrier of the pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int x, int y) {
   asm volatile(
-      "{ .reg .pred p; .reg .b64 da, db; mov.b64 da, {%1, %3}; mov.b64 db, {%2, %3};"
-      " setp.ne.b32 p, %5, 0;"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %4, p; }" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
+      : "memory");
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
       : "memory");
 }
 
-// SiLU in fp32 accuracy: the product's callers compare it with the definition, and its
-// rounding to bf16 is the only one.
-__device__ __forceinline__ float silu_full(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+constexpr float kLog2E = 1.44269504088896341f;
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// SiLU of two values with one reciprocal: 1/a = b / (a b).  The exponentials are held below
+// 2^63 (x > -43.6) so that a b stays finite; beyond that |SiLU| < 5e-18 is off by no more than
+// that.  Otherwise within a few roundings of fp32: bf16's rounding is the only visible one.
+__device__ __forceinline__ void silu2(float& x0, float& x1) {
+  const float a = 1.f + fminf(ex2_approx(x0 * -kLog2E), 0x1p63f), b = 1.f + fminf(ex2_approx(x1 * -kLog2E), 0x1p63f);
+  const float r = rcp_approx(a * b);
+  x0 = x0 * (r * b);
+  x1 = x1 * (r * a);
+}
 
-// 32 consecutive columns of one output row.
+// act, and the residual of a row whose 32 columns start at col.
 template <typename OT>
-__device__ __forceinline__ void store_row32(const Args& p, int row, int col, float (&v)[32]) {
+__device__ __forceinline__ void finish32(const Args& p, int64_t orow, int col, float (&v)[32]) {
   const Fp8Epi& e = p.epi;
   if (e.act == MTFM_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = silu_full(v[j]);
+    for (int j = 0; j < 32; j += 2) silu2(v[j], v[j + 1]);
   }
-  const int64_t orow = e.row_map ? e.row_map[row] : row;
+  if (!e.res) return;
   const int n = p.N - col;
-  if (e.res) {
-    const OT* r = static_cast<const OT*>(e.res) + orow * e.ld_res + col;
-    if (p.vec && n >= 32) {
-      if constexpr (sizeof(OT) == 4) {
+  const OT* r = static_cast<const OT*>(e.res) + orow * e.ld_res + col;
+  if (p.vec && n >= 32) {
+    if constexpr (sizeof(OT) == 4) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 t = reinterpret_cast<const float4*>(r)[j];
-          v[4 * j] += t.x; v[4 * j + 1] += t.y; v[4 * j + 2] += t.z; v[4 * j + 3] += t.w;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 t = reinterpret_cast<const uint4*>(r)[j];
-          const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            v[8 * j + 2 * k] += __uint_as_float(w[k] << 16);
-            v[8 * j + 2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
-          }
-        }
+      for (int j = 0; j < 8; ++j) {
+        const float4 t = reinterpret_cast<const float4*>(r)[j];
+        v[4 * j] += t.x; v[4 * j + 1] += t.y; v[4 * j + 2] += t.z; v[4 * j + 3] += t.w;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) v[j] += (float)r[j];
+      for (int j = 0; j < 4; ++j) {
+        const uint4 t = reinterpret_cast<const uint4*>(r)[j];
+        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[8 * j + 2 * k] += __uint_as_float(w[k] << 16);
+          v[8 * j + 2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
+        }
+      }
     }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) v[j] += (float)r[j];
   }
+}
+
+// 32 finished columns of one row, stored directly.
+template <typename OT>
+__device__ __forceinline__ void store32(const Args& p, int64_t orow, int col, const float (&v)[32]) {
+  const Fp8Epi& e = p.epi;
   void* base = e.seg_ptr[0];
   int64_t ld = e.seg_ld[0];
   int c0 = 0;
@@ -119,6 +222,7 @@ __device__ __forceinline__ void store_row32(const Args& p, int row, int col, flo
       ld = e.seg_ld[s];
       c0 = e.seg_begin[s];
     }
+  const int n = p.N - col;
   OT* o = static_cast<OT*>(base) + orow * ld + (col - c0);
   if (p.vec && n >= 32) {
     if constexpr (sizeof(OT) == 4) {
@@ -139,44 +243,73 @@ __device__ __forceinline__ void store_row32(const Args& p, int row, int col, flo
   }
 }
 
-template <int BN, typename OT>
-__global__ void __launch_bounds__(kThreadsG, 1)
-gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, Args p) {
-  constexpr int kStages = stages_g<BN>(), kAcc = acc_bufs<BN>();
-  constexpr uint32_t kStage = stage_bytes_g<BN>();
-  constexpr uint32_t kTmemCols = kAcc * BN;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages];
-  __shared__ __align__(8) uint64_t bar_acc_full[kAcc], bar_acc_empty[kAcc], bar_drain;
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+__device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nN = (p.N + BN - 1) / BN, nK = (p.K + kGroup - 1) / kGroup;
-  const int64_t n_tiles = (int64_t)((p.M + kBM - 1) / kBM) * nN;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+// 4-byte asynchronous copy global -> shared, zero-filled past `bytes`; and an arrival on an
+// mbarrier once this thread's copies so far have landed.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// First row and column of tile t: bands of n_group tile columns, walked row by row, so that
+// the pairs at work share a band of B and few rows of A in L2.
+struct Tile {
+  int m0, n0;
+};
+template <int BN>
+__device__ __forceinline__ Tile tile_at(const Args& p, int t, int nM, int nN) {
+  const int band = nM * p.n_group;
+  const int b = t / band;
+  const int in = t - b * band;
+  const int w = min(p.n_group, nN - b * p.n_group);
+  const int m = in / w;
+  return {m * (2 * kBM), (b * p.n_group + in - m * w) * BN};
+}
+
+// TMA_OUT: the output leaves through 128-byte wide boxes staged in shared memory and TMA
+// stores (whole 16-byte aligned rows, one segment per map, no row map).
+template <int BN, typename OT, bool TMA_OUT>
+__global__ void __launch_bounds__(kThreadsG, 1)
+gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                const __grid_constant__ CUtensorMap tm_o0, const __grid_constant__ CUtensorMap tm_o1,
+                const __grid_constant__ CUtensorMap tm_o2, const __grid_constant__ CUtensorMap tm_o3,
+                const __grid_constant__ Args p) {
+  constexpr int kStages = stages_g<BN>(), kParts = parts_g<BN>(), kAcc = acc_bufs<BN>();
+  constexpr uint32_t kStage = stage_bytes_g<BN>();
+  constexpr uint32_t kTmemCols = 512;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + bars_off<BN>());
+
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int nM = (p.M + 2 * kBM - 1) / (2 * kBM), nN = (p.N + BN - 1) / BN, nK = (p.K + kGroup - 1) / kGroup;
+  const int n_tiles = nM * nN;  // (an output of 2^31 tiles does not fit in memory)
+  const int step = (int)(gridDim.x >> 1);
   const uint32_t sbase = smem_addr(smem);
-  auto b_full = [&](int s) { return smem_addr(&bar_full[s]); };
-  auto b_empty = [&](int s) { return smem_addr(&bar_empty[s]); };
-  auto b_accf = [&](int a) { return smem_addr(&bar_acc_full[a]); };
-  auto b_acce = [&](int a) { return smem_addr(&bar_acc_empty[a]); };
-  const uint32_t b_drain = smem_addr(&bar_drain);
+  const uint32_t b_full = smem_addr(bars.full), b_empty = smem_addr(bars.empty);
+  const uint32_t b_accf = smem_addr(bars.acc_full), b_acce = smem_addr(bars.acc_empty);
+  const uint32_t b_scf = smem_addr(bars.sc_full), b_sce = smem_addr(bars.sc_empty);
   if (threadIdx.x == 0) {
-    s_abort = 0;
+    bars.abort = 0;
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(b_full(s), 1);
-      mbar_init(b_empty(s), 1);
+      mbar_init(b_full + s * 8, 1);
+      mbar_init(b_empty + s * 8, kParts);  // one commit of each part's issuer
     }
-    for (int a = 0; a < kAcc; ++a) {
-      mbar_init(b_accf(a), 1);
-      mbar_init(b_acce(a), kEpiWarps);
-    }
-    mbar_init(b_drain, 1);
+    // a buffer is announced to the set of warpgroups whose tile it belongs to (a waiting set must
+    // not miss a phase of its barrier while the other set's tile goes through the buffers)
+    for (int a = 0; a < 2 * kAcc; ++a) mbar_init(b_accf + a * 8, 1);
+    for (int a = 0; a < kParts * kAcc; ++a) mbar_init(b_acce + a * 8, 16);  // two warpgroups of both CTAs
+    for (int a = 0; a < 2 * kSlots; ++a) mbar_init(b_scf + a * 8, 32);      // the lanes of warp 2
+    for (int a = 0; a < kSlots; ++a) mbar_init(b_sce + a * 8, 8 * kParts);  // the warps of the tile's set
+    mbar_init(smem_addr(&bars.drain[0]), 1);
+    mbar_init(smem_addr(&bars.drain[1]), 1);
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_addr(&s_tmem), kTmemCols);
-    tmem_relinquish();
+    tmem_alloc2(smem_addr(&bars.tmem), kTmemCols);
     tc_fence_before();
   }
   if (warp == 0 && lane == 0) {
@@ -184,136 +317,278 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     tma_prefetch_desc(&tm_b);
   }
   pdl_wait();
-  // an earlier kernel on this error word failed: nothing is loaded or stored (TMEM is freed below)
-  const bool skip = *p.err != 0;
+  // an earlier kernel on this error word failed: nothing is loaded or stored (the pair goes by
+  // the leader's reading of it)
+  if (threadIdx.x == 0) {
+    if (sbase & 1023) bars.abort = 1;  // the swizzled tiles need what the declaration asks for
+    bars.skip = *p.err != 0 || (sbase & 1023) != 0;
+  }
   __syncthreads();
+  cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
-  volatile int* abort_flag = &s_abort;
-  const int64_t first = skip ? n_tiles : (int64_t)blockIdx.x;
+  const uint32_t tmem = bars.tmem;
+  volatile int* abort_flag = &bars.abort;
+  const bool skip = ld_cluster(map_rank(smem_addr(&bars.skip), 0)) != 0;
+  const int first = skip ? n_tiles : (int)(blockIdx.x >> 1);
 
   if (warp < 4) {
-    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0 && lane == 0) {
-      // ----------------------------------------------------------- TMA producer
-      int64_t G = 0;  // K blocks issued by this CTA (ring position and phase)
+      // ----------------------------------------------------------- TMA producer (each CTA)
+      int s = 0;
+      uint32_t phase = 0;  // of the stage's use (waiting for the phase before the first returns at once)
+      const uint32_t full0 = map_rank((b_full + 0 * 8), 0);
       bool ok = true;
-      for (int64_t t = first; ok && t < n_tiles; t += gridDim.x) {
-        const int m0 = (int)(t / nN) * kBM, n0 = (int)(t % nN) * BN;
-        for (int kb = 0; kb < nK; ++kb, ++G) {
-          const int s = (int)(G % kStages);
-          if (G >= kStages && !mbar_wait(b_empty(s), (uint32_t)((G / kStages) - 1) & 1, abort_flag)) {
+      int64_t issued = 0;
+      for (int t = first; ok && t < n_tiles; t += step) {
+        const Tile tl = tile_at<BN>(p, t, nM, nN);
+        const int m0 = tl.m0 + (int)rank * kBM, n0 = tl.n0 + (int)rank * 64;
+        for (int kb = 0; kb < nK; ++kb) {
+          if (!mbar_wait((b_empty + s * 8), phase ^ 1, abort_flag)) {
             ok = false;
             break;
           }
-          // boxes that reach past the matrix are filled with zeros and count in full
-          mbar_expect_tx(b_full(s), kStage);
-          tma_load_2d(sbase + s * kStage, &tm_a, b_full(s), kb * kGroup, m0);
-          tma_load_2d(sbase + s * kStage + kABytes, &tm_b, b_full(s), kb * kGroup, n0);
+          const uint32_t full = full0 + (uint32_t)s * 8;
+          // boxes that reach past a matrix are filled with zeros and count in full
+          if (rank == 0) mbar_expect_tx((b_full + s * 8), 2 * kStage);
+          tma_load_pair(sbase + s * kStage, &tm_a, full, kb * kGroup, m0);
+#pragma unroll
+          for (int part = 0; part < kParts; ++part)  // this CTA's 64 of the part's 128 rows of B
+            tma_load_pair(sbase + s * kStage + kABytes + part * (64 * kGroup), &tm_b, full, kb * kGroup, n0 + part * 128);
+          ++issued;
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
       }
-      // no copy may land after the CTA leaves: wait (bounded) for the last one of each stage
-      const long long t0 = clock64();
-      for (int64_t g = G > kStages ? G - kStages : 0; g < G; ++g)
-        while (!mbar_try(b_full((int)(g % kStages)), (uint32_t)(g / kStages) & 1) && clock64() - t0 < kWaitCycles) {
-        }
-    } else if (warp == 1) {
-      // ----------------------------------------------------------- MMA issuer
-      constexpr uint32_t idesc = idesc_e4m3_f32(kBM, BN);
-      const uint32_t dhi = sw128_desc_hi(1024);
-      const uint32_t a_lo = sw128_desc_lo(sbase, 16), b_lo = sw128_desc_lo(sbase + kABytes, 16);
+      // no copy may land after the pair leaves: the leader, whose barriers count both CTAs'
+      // copies, waits (bounded) for the last one of each stage
+      if (rank == 0) {
+        const long long t0 = clock64();
+        for (int64_t g = issued > kStages ? issued - kStages : 0; g < issued; ++g)
+          while (!mbar_try(b_full + (uint32_t)(g % kStages) * 8, (uint32_t)(g / kStages) & 1) && clock64() - t0 < kWaitCycles) {
+          }
+      }
+    } else if (rank == 0 && (warp == 1 || (warp == 3 && kParts > 1))) {
+      // ----------------------------------------------------------- MMA issuers (leader), one a part
+      constexpr uint32_t idesc = idesc_e4m3_f32(2 * kBM, 128);
+      const int part = warp >> 1;
+      const uint64_t a_desc = sw128_desc(sbase, 16, 1024);
+      const uint64_t b_desc = sw128_desc(sbase + kABytes + part * (64 * kGroup), 16, 1024);
+      const uint32_t b_drain = smem_addr(&bars.drain[part]);
       bool ok = true;
-      int64_t G = 0;
-      for (int64_t t = first; ok && t < n_tiles; t += gridDim.x) {
-        for (int kb = 0; kb < nK; ++kb, ++G) {
-          const int s = (int)(G % kStages), a = (int)(G % kAcc);
-          ok = (G < kAcc || mbar_wait(b_acce(a), (uint32_t)((G / kAcc) - 1) & 1, abort_flag)) &&
-               mbar_wait(b_full(s), (uint32_t)(G / kStages) & 1, abort_flag);
+      int s = 0, set = 0;  // set: whose tile it is (BN = 128)
+      uint32_t ph_s = 0, n = 0;  // n: blocks issued: buffer n % kAcc, round n / kAcc
+      for (int t = first; ok && t < n_tiles; t += step, set ^= 1) {
+        for (int kb = 0; kb < nK; ++kb, ++n) {
+          const int a = (int)(n % kAcc);
+          ok = mbar_wait((b_full + s * 8), ph_s, abort_flag) && mbar_wait(b_acce + (uint32_t)(part * kAcc + a) * 8, (n / kAcc - 1) & 1, abort_flag);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t ao = a_lo + s * (kStage >> 4), bo = b_lo + s * (kStage >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kGroup / 32; ++kk)
-              mma_f8(tmem + (uint32_t)(a * BN), ao + kk * 2, bo + kk * 2, dhi, idesc, kk > 0 ? 1u : 0u);
-            mma_commit(b_empty(s));
-            mma_commit(b_accf(a));
+            const uint64_t ad = a_desc + (uint32_t)(s * (kStage >> 4)), bd = b_desc + (uint32_t)(s * (kStage >> 4));
+            const uint32_t d = tmem + (uint32_t)((part * kAcc + a) * 128);
+            mma_f8_pair<false>(d, ad, bd, idesc);  // 32 columns of K each
+            mma_f8_pair<true>(d, ad + 2, bd + 2, idesc);
+            mma_f8_pair<true>(d, ad + 4, bd + 4, idesc);
+            mma_f8_pair<true>(d, ad + 6, bd + 6, idesc);
+            commit_pair(b_accf + (uint32_t)((kParts > 1 ? part : set) * kAcc + a) * 8);
+            commit_pair((b_empty + s * 8));
           }
           __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            ph_s ^= 1;
+          }
         }
       }
       if (!ok) {
         // drain every MMA issued so far before TMEM is released
-        if (elect_one()) mma_commit(b_drain);
+        if (elect_one()) commit_pair(b_drain);
         __syncwarp();
         const long long t0 = clock64();
         while (!mbar_try(b_drain, 0) && clock64() - t0 < kWaitCycles) {
         }
       }
+    } else if (warp == 2) {
+      // ----------------------------------------------------------- A scales (each CTA): lane l
+      // copies rows l, l + 32, l + 64, l + 96 of a block; rows past M become 0
+      bool ok = true;
+      int slot = 0, set = 0;
+      uint32_t ph = 0;
+      for (int t = first; ok && t < n_tiles; t += step, set ^= 1) {
+        const int row = tile_at<BN>(p, t, nM, nN).m0 + (int)rank * kBM + lane;
+        const float* src = p.sa + (int64_t)row * p.ld_sa;
+        for (int kb = 0; kb < nK; ++kb) {
+          if (!__all_sync(0xffffffffu, mbar_wait(b_sce + slot * 8, ph ^ 1, abort_flag))) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sbase + scale_off<BN>() + (uint32_t)(slot * 128 + lane) * 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool in = row + 32 * i < p.M;
+            copy4(dst + i * 128, in ? src + (int64_t)(32 * i) * p.ld_sa + kb : p.sa, in ? 4 : 0);
+          }
+          copy_arrive(b_scf + (uint32_t)((kParts > 1 ? 0 : set) * kSlots + slot) * 8);
+          if (++slot == kSlots) {
+            slot = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ------------------------------------------------------------- scaling and epilogue
-    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    constexpr int kHalf = BN / 2, kChunks = kHalf / 32;
-    const int quad = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t tlane = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * kHalf);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+    constexpr int kSets = 256 / BN;  // sets of warpgroups that take turns on tiles
+    const int quad = warp & 3, wg = (warp - 4) >> 2;
+    const int r_in = quad * 32 + lane;
+    const int set = kSets > 1 ? wg >> 1 : 0;
+    const int part = kParts > 1 ? wg >> 1 : 0;
+    const int tcol = kSets > 1 ? (wg & 1) * kCols : wg * kCols;  // first column within the tile
+    const uint32_t tlane = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(part * (kAcc * 128) + (wg & 1) * kCols);
+    uint8_t* stage = smem + stage_off<BN>() + wg * kBoxBytes;
+    const uint32_t sstage = smem_addr(stage);
+    const int bar_id = 2 + wg;
+    const uint32_t accf0 = b_accf + (uint32_t)((wg >> 1) * kAcc) * 8;            // BN = 256: by part; 128: by set
+    const uint32_t acce0 = map_rank(b_acce + (uint32_t)(part * kAcc) * 8, 0);  // (mapped once: mapa in the loop cost 140 cycles a block)
+    const bool issuer = quad == 0 && lane == 0;
     bool ok = true;
-    int64_t G = 0;
-    for (int64_t t = first; ok && t < n_tiles; t += gridDim.x) {
-      const int row = (int)(t / nN) * kBM + quad * 32 + lane;
-      const int col0 = (int)(t % nN) * BN + half * kHalf;
-      const float* sa = p.sa + (int64_t)(row < p.M ? row : 0) * p.ld_sa;
-      // the warpgroup's columns lie in one 128-row block of B; columns past N read no scale of their own
+    uint32_t n = (uint32_t)(set * nK);  // blocks before this set's next one: buffer n % kAcc
+    uint32_t phases = 0;                // of this set's barriers, one bit a buffer
+    const uint32_t scf0 = b_scf + (uint32_t)((kParts > 1 ? 0 : set) * kSlots) * 8;
+    const volatile float* s_scale = reinterpret_cast<const volatile float*>(smem + scale_off<BN>());
+    int slot = set * nK % kSlots;
+    uint32_t sc_phases = 0;
+    for (int t = first + set * step; ok && t < n_tiles; t += kSets * step, n += (uint32_t)((kSets - 1) * nK), slot = (slot + (kSets - 1) * nK) % kSlots) {
+      const Tile tl = tile_at<BN>(p, t, nM, nN);
+      const int m0 = tl.m0 + (int)rank * kBM;
+      const int row = m0 + r_in;
+      const int col0 = tl.n0 + tcol;
+      // the warpgroup's columns lie in one 128-row block of B; columns past N have no scale of their own
       const float* sb = p.sb + (int64_t)((col0 < p.N ? col0 : p.N - 1) / kGroup) * p.ld_sb;
-      float acc[kHalf];
+      float2 acc[kCols / 2];
 #pragma unroll
-      for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
-      float sa_next = sa[0], sb_next = sb[0];
-      for (int kb = 0; kb < nK; ++kb, ++G) {
-        const int a = (int)(G % kAcc);
-        const float sc = sa_next * sb_next;
-        if (kb + 1 < nK) {
-          sa_next = sa[kb + 1];
-          sb_next = sb[kb + 1];
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(b_accf(a), (uint32_t)(G / kAcc) & 1, abort_flag))) {
+      for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      float sb_next = sb[0];
+      for (int kb = 0; kb < nK; ++kb, ++n) {
+        if (!__all_sync(0xffffffffu, mbar_wait(scf0 + (uint32_t)slot * 8, (sc_phases >> slot) & 1, abort_flag))) {
           ok = false;
           break;
         }
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          uint32_t raw[32];
-          tmem_ld32(tlane + (uint32_t)(a * BN + c * 32), raw);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) acc[c * 32 + j] = fmaf(__uint_as_float(raw[j]), sc, acc[c * 32 + j]);
-        }
-        tc_fence_before();
+        const float sc = s_scale[slot * 128 + r_in] * sb_next;
+        if (kb + 1 < nK) sb_next = sb[kb + 1];
+        sc_phases ^= 1u << slot;
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_acce(a));
+        if (lane == 0) mbar_arrive(b_sce + (uint32_t)slot * 8);
+        slot = slot + 1 == kSlots ? 0 : slot + 1;
+        const int a = (int)(n % kAcc);
+        if (!__all_sync(0xffffffffu, mbar_wait(accf0 + (uint32_t)a * 8, (phases >> a) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        phases ^= 1u << a;
+        tc_fence_after();
+        const uint32_t ta = tlane + (uint32_t)(a * 128);
+        const float2 s2 = make_float2(sc, sc);
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          uint32_t raw[32];
+          tmem_ld32(ta + (uint32_t)(c * 32), raw);
+          tmem_ld_wait();
+          if (c + 1 == kCols / 32) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acce0 + (uint32_t)a * 8);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            acc[c * 16 + j] = __ffma2_rn(make_float2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])), s2,
+                                         acc[c * 16 + j]);
+        }
       }
-      if (ok && row < p.M) {
+      if (TMA_OUT) {
+        // uniform over the warpgroup before its barriers
+        uint32_t all;
+        asm volatile(
+            "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.and.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
+            : "=r"(all) : "r"((uint32_t)ok), "r"(bar_id) : "memory");
+        ok = all != 0;
+      }
+      if (!ok) break;
+      const int64_t orow = row < p.M ? (p.epi.row_map ? p.epi.row_map[row] : row) : 0;
+      if constexpr (TMA_OUT) {
+        constexpr int kBoxCols = 128 / (int)sizeof(OT);  // 64 bf16 or 32 fp32
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          float v[32];
+        for (int b = 0; b < kCols / kBoxCols; ++b) {
+          if (issuer) bulk_wait_read<0>();  // the last store has read the staging
+          wg_sync(bar_id);
+          uint8_t* rowp = stage + r_in * 128;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = acc[c * 32 + j];
-          if (col0 + c * 32 < p.N) store_row32<OT>(p, row, col0 + c * 32, v);
+          for (int c = 0; c < kBoxCols / 32; ++c) {
+            const int col = b * kBoxCols + c * 32;  // within the warpgroup's columns
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[2 * j] = acc[col / 2 + j].x, v[2 * j + 1] = acc[col / 2 + j].y;
+            if (row < p.M && col0 + col < p.N) finish32<OT>(p, orow, col0 + col, v);
+#pragma unroll
+            for (int i = 0; i < 2 * (int)sizeof(OT); ++i) {
+              const int chunk = c * 2 * (int)sizeof(OT) + i;
+              uint4 w;
+              if constexpr (sizeof(OT) == 4)
+                w = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                               __float_as_uint(v[4 * i + 3]));
+              else
+                w = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                               pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+              *reinterpret_cast<uint4*>(rowp + ((chunk ^ (r_in & 7)) << 4)) = w;
+            }
+          }
+          fence_proxy_async();
+          wg_sync(bar_id);
+          const int col = col0 + b * kBoxCols;
+          if (issuer && m0 < p.M && col < p.N) {
+            const CUtensorMap* om = &tm_o0;
+            int begin = 0;
+#pragma unroll
+            for (int q = 1; q < 4; ++q)
+              if (q < p.epi.n_seg && col >= p.epi.seg_begin[q]) {
+                begin = p.epi.seg_begin[q];
+                om = q == 1 ? &tm_o1 : q == 2 ? &tm_o2 : &tm_o3;
+              }
+            tma_store_2d(om, sstage, col - begin, m0);
+            bulk_commit();
+          }
+        }
+      } else if (row < p.M) {
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          if (col0 + c * 32 < p.N) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[2 * j] = acc[c * 16 + j].x, v[2 * j + 1] = acc[c * 16 + j].y;
+            finish32<OT>(p, orow, col0 + c * 32, v);
+            store32<OT>(p, orow, col0 + c * 32, v);
+          }
         }
       }
     }
+    if (TMA_OUT && issuer) bulk_wait<0>();  // every store has completed before the CTA leaves
   }
   pdl_trigger();
   __syncthreads();
+  cluster_sync();  // the other CTA's MMAs, copies and arrivals reach into this one
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc2(tmem, kTmemCols);
   }
-  if (threadIdx.x == 0 && s_abort) atomicOr(p.err, kErrTimeout);
+  if (threadIdx.x == 0 && bars.abort) atomicOr(p.err, kErrTimeout);
 }
 
 // Row-major e4m3 matrix [rows, cols], row pitch ld bytes; boxes of box_rows x 128 columns.
@@ -328,18 +603,62 @@ bool make_map_e4m3(CUtensorMap* map, const uint8_t* base, int rows, int cols, in
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// Output matrix [rows, cols] in boxes of 128 rows x 128 bytes.
+bool make_map_out(CUtensorMap* map, void* base, int type, int rows, int cols, int64_t ld) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int size = dtype_size(type);
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld * size)};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)kBM};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, type == MTFM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
-template <int BN, typename OT>
-cudaError_t go(const Fp8In& a, const Fp8In& b, const Args& args, cudaStream_t st) {
-  CUtensorMap ma, mb;
-  if (!make_map_e4m3(&ma, a.q, args.M, args.K, a.ld, kBM) || !make_map_e4m3(&mb, b.q, args.N, args.K, b.ld, BN))
-    return cudaErrorInvalidValue;
+template <int BN, typename OT, bool TMA_OUT>
+cudaError_t go(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap (&mo)[4], const Args& args, int64_t tiles,
+               cudaStream_t st) {
+  auto kern = gemm_fp8_kernel<BN, OT, TMA_OUT>;
   const size_t smem = smem_g<BN>();
-  cudaError_t e = cudaFuncSetAttribute(gemm_fp8_kernel<BN, OT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((int64_t)args.M + kBM - 1) / kBM * (((int64_t)args.N + BN - 1) / BN);
-  return launch_pdl(gemm_fp8_kernel<BN, OT>, dim3((unsigned)std::min<int64_t>(tiles, sm_count())), dim3(kThreadsG), smem, st,
-                    ma, mb, args);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(tiles, sm_count() / 2));
+  cfg.blockDim = dim3(kThreadsG);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, mo[0], mo[1], mo[2], mo[3], args);
+}
+
+template <int BN>
+cudaError_t launch(const Fp8In& a, const Fp8In& b, Args& args, cudaStream_t st) {
+  CUtensorMap ma, mb, mo[4];
+  memset(mo, 0, sizeof(mo));
+  if (!make_map_e4m3(&ma, a.q, args.M, args.K, a.ld, kBM) || !make_map_e4m3(&mb, b.q, args.N, args.K, b.ld, 64))
+    return cudaErrorInvalidValue;
+  const Fp8Epi& e = args.epi;
+  const int box_cols = 128 / dtype_size(e.out_type);
+  bool tma = args.vec && !e.row_map;
+  // a TMA store writes whole 16-byte pieces of a row: a row that ends inside one is stored directly
+  for (int s = 0; s < e.n_seg && tma; ++s)
+    tma = e.seg_begin[s] % box_cols == 0 && (e.seg_begin[s + 1] - e.seg_begin[s]) * dtype_size(e.out_type) % 16 == 0 &&
+          make_map_out(&mo[s], e.seg_ptr[s], e.out_type, args.M, e.seg_begin[s + 1] - e.seg_begin[s], e.seg_ld[s]);
+  const int64_t nM = ((int64_t)args.M + 2 * kBM - 1) / (2 * kBM), nN = ((int64_t)args.N + BN - 1) / BN;
+  args.n_group = (int)std::min<int64_t>(nN, 8);
+  if (e.out_type == MTFM_BF16)
+    return tma ? go<BN, __nv_bfloat16, true>(ma, mb, mo, args, nM * nN, st)
+               : go<BN, __nv_bfloat16, false>(ma, mb, mo, args, nM * nN, st);
+  return tma ? go<BN, float, true>(ma, mb, mo, args, nM * nN, st) : go<BN, float, false>(ma, mb, mo, args, nM * nN, st);
 }
 
 }  // namespace
@@ -353,8 +672,9 @@ cudaError_t launch_gemm_fp8(int32_t* err, int M, int N, int K, const Fp8In& a, c
   };
   bool vec = !epi.res || rows16(epi.res, epi.ld_res);
   for (int s = 0; s < epi.n_seg; ++s) vec = vec && rows16(epi.seg_ptr[s], epi.seg_ld[s]);
-  const Args args{err, M, N, K, a.scale, a.ld_scale, b.scale, b.ld_scale, epi, vec};
-  return epi.out_type == MTFM_BF16 ? go<128, __nv_bfloat16>(a, b, args, st) : go<128, float>(a, b, args, st);
+  Args args{err, M, N, K, a.scale, a.ld_scale, b.scale, b.ld_scale, epi, 1, vec};
+  const int64_t tiles256 = (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256);
+  return tiles256 >= sm_count() / 2 ? launch<256>(a, b, args, st) : launch<128>(a, b, args, st);
 }
 
 }  // namespace mtfm

@@ -302,7 +302,9 @@ def check_gemm(out, a, sa, b, sb, act, res):
 
 SHAPES = [(1, 1, 1), (1, 128, 128), (2, 17, 33), (5, 1280, 512), (16, 300, 1000), (33, 1000, 129), (64, 64, 2000),
           (65, 512, 4096), (127, 255, 384), (128, 256, 256), (129, 257, 130), (300, 1000, 1000), (1000, 33, 640),
-          (777, 1280, 512), (2049, 640, 96), (1, 5000, 8192), (40, 2048, 8190)]
+          (777, 1280, 512), (2049, 640, 96), (1, 5000, 8192), (40, 2048, 8190),
+          # more tiles than CTA pairs: 256 x 128 and 256 x 256 tiles, short and long K
+          (2200, 2000, 512), (2200, 2000, 130), (2200, 1990, 1100), (5000, 2048, 512), (5000, 2050, 130), (4500, 2100, 1300)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
