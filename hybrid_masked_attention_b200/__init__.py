@@ -38,6 +38,12 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+try:
+    from . import _fastcall
+except ImportError as e:
+    raise ImportError("_fastcall.so not found or not loadable; build it with "
+                      "`python hybrid_masked_attention_b200/build.py`") from e
+
 MTFM_OK = 0
 STATUS_NAMES = {
     0: "MTFM_OK", 1: "MTFM_ERR_INVALID_ARG", 2: "MTFM_ERR_UNSORTED_TS", 3: "MTFM_ERR_UNSUPPORTED",
@@ -576,6 +582,14 @@ _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 _ACTS = {None: 0, "silu": 1}
 FP8_GROUP = 128
 
+# The wrappers below first offer a call to csrc/fastcall.c, which reads the same attributes,
+# makes the same checks and calls the entry point; it declines (None) whatever does not hold,
+# and the checks here then say what.
+_entry = lambda name: ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value
+_fastcall.setup(torch.float32, torch.bfloat16, _F8, torch.uint8, torch.int32, torch._C._cuda_getDevice,
+                torch._C._cuda_getCurrentRawStream, *map(_entry, (
+                    "mtfm_add_rmsnorm_fp8", "mtfm_rmsnorm_bwd", "mtfm_gate_fwd_fp8", "mtfm_fp8_quant", "mtfm_fp8_gemm")))
+
 
 def _groups(n: int) -> int:
     return -(-n // FP8_GROUP)
@@ -636,6 +650,12 @@ def add_rmsnorm_fp8(x, delta, weight, x_out, out, scale, rstd=None, eps=0.0, str
     x fp32 or bf16 [rows, dim]; delta fp32 or bf16, or None (then x_out is None); x_out may be x,
     or None; weight fp32 [dim]; out float8_e4m3fn [rows, dim]; scale fp32 [rows, ceil(dim / 128)];
     rstd fp32 [rows] or None; eps <= 0 selects 1e-6."""
+    if stream is None:
+        st = _fastcall.add_rmsnorm_fp8(x, delta, weight, x_out, out, scale, rstd, float(eps))
+        if st == MTFM_OK:
+            return
+        if st is not None:
+            raise MtfmError(st, "mtfm_add_rmsnorm_fp8")
     dev = _device_of(x, "x")
     rows, dim = x.shape
     px, ldx = _mat(x, "x", dev, rows, dim)
@@ -660,6 +680,12 @@ def rmsnorm_bwd(x, weight, rstd, dy, dres, dx, dw, ws, stream=None):
 
     x: the normalised stream (add_rmsnorm_fp8's x_out) with its rstd; dx has x's type and may be dy
     or dres; ws: uint8 of rmsnorm_bwd_workspace_bytes(rows, dim), not shared by overlapping calls."""
+    if stream is None:
+        st = _fastcall.rmsnorm_bwd(x, weight, rstd, dy, dres, dx, dw, ws)
+        if st == MTFM_OK:
+            return
+        if st is not None:
+            raise MtfmError(st, "mtfm_rmsnorm_bwd")
     dev = _device_of(x, "x")
     rows, dim = x.shape
     px, ldx = _mat(x, "x", dev, rows, dim)
@@ -674,6 +700,13 @@ def rmsnorm_bwd(x, weight, rstd, dy, dres, dx, dw, ws, stream=None):
 
 def gate_fwd_fp8(cfg, meta, target: bool, a, u, gamma, beta, out, scale, stats, stream=None):
     """gate_fwd with its output in 8 bits: (out, scale) = groups of GLN(A) (*) U."""
+    c = cfg.c()
+    if stream is None:
+        st = _fastcall.gate_fwd_fp8(ctypes.addressof(c), meta, target, a, u, gamma, beta, out, scale, stats)
+        if st == MTFM_OK:
+            return
+        if st is not None:
+            raise MtfmError(st, "mtfm_gate_fwd_fp8")
     rows, D = cfg.total_t if target else cfg.total_tokens, cfg.D
     dev = _device_of(a, "a")
     for t, name in ((meta, "meta"), (u, "u"), (gamma, "gamma"), (beta, "beta"), (stats, "stats")):
@@ -681,7 +714,6 @@ def gate_fwd_fp8(cfg, meta, target: bool, a, u, gamma, beta, out, scale, stats, 
             raise ValueError(f"{name} must be on device {dev}, got {t.device}")
     pq, ldq = _mat(out, "out", dev, rows, D, _F8)
     ps, lds = _mat(scale, "scale", dev, rows, _groups(D), _F32)
-    c = cfg.c()
     _run_on(dev, stream, "mtfm_gate_fwd_fp8", _lib.mtfm_gate_fwd_fp8, ctypes.byref(c), _ptr(meta, torch.uint8, None, "meta"),
             int(bool(target)), _ptr(a, _F32, (rows, D), "a"), _ptr(u, torch.bfloat16, (rows, D), "u"),
             _ptr(gamma, _F32, (3, D), "gamma"), _ptr(beta, _F32, (3, D), "beta"), pq, ldq, ps, lds,
@@ -690,6 +722,12 @@ def gate_fwd_fp8(cfg, meta, target: bool, a, u, gamma, beta, out, scale, stats, 
 
 def fp8_quant(x, out, scale, block_rows: int = 1, stream=None):
     """(out, scale) = x in 8 bits, one scale per 1 x 128 group (block_rows 1) or 128 x 128 block (128)."""
+    if stream is None:
+        st = _fastcall.fp8_quant(x, out, scale, block_rows)
+        if st == MTFM_OK:
+            return
+        if st is not None:
+            raise MtfmError(st, "mtfm_fp8_quant")
     dev = _device_of(x, "x")
     rows, cols = x.shape
     if block_rows not in (1, FP8_GROUP):
@@ -707,6 +745,12 @@ def fp8_gemm(a, a_scale, b, b_scale, out, status, act: Optional[str] = None, res
     act None or "silu"; out fp32 or bf16; residual None or a matrix of out's type (out itself
     allowed); a and b start on 16-byte boundaries with row pitches that are multiples of 16;
     status: int32 [1], zeroed once (fp8_check reads it)."""
+    if stream is None:
+        st = _fastcall.fp8_gemm(a, a_scale, b, b_scale, out, status, _ACTS.get(act, -1), residual)
+        if st == MTFM_OK:
+            return
+        if st is not None:
+            raise MtfmError(st, "mtfm_fp8_gemm")
     dev = _device_of(a, "a")
     _device_of(b, "b")
     m, k = a.shape

@@ -4,8 +4,9 @@
 
 Each .cu under csrc/ is compiled to an object in parallel with
 ``nvcc -gencode arch=compute_100a,code=sm_100a -lineinfo -O3``, then linked
-into ``hybrid_masked_attention_b200/libmtfm.so``.  Rebuilds only when a source
-or header is newer than the library.
+into ``hybrid_masked_attention_b200/libmtfm.so``; csrc/fastcall.c, the argument
+marshalling of the 8-bit operators, becomes ``_fastcall.so`` beside it (gcc, CPython's
+headers).  Rebuilds only when a source or header is newer than the library.
 
     python hybrid_masked_attention_b200/build.py --debug-bounds
 
@@ -23,12 +24,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmtfm.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 DEBUG_BUILD = os.path.join(PKG, "_build_debug_bounds")
 DEBUG_LIB = os.path.join(PKG, "libmtfm_debug_bounds.so")
 INCLUDE = os.path.join(ROOT, "include")
@@ -73,7 +76,23 @@ def _compile(src: str, verbose: bool, extra, build_dir: str = BUILD) -> str:
     return obj
 
 
+def build_fastcall(force: bool = False) -> str:
+    src = os.path.join(CSRC, "fastcall.c")
+    deps = (src, os.path.join(INCLUDE, "mtfm.h"))
+    if not force and os.path.exists(FASTCALL) and all(os.path.getmtime(d) <= os.path.getmtime(FASTCALL) for d in deps):
+        return FASTCALL
+    tmp = FASTCALL + ".tmp"
+    cmd = [os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared", "-fPIC",
+           "-I", sysconfig.get_paths()["include"], src, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {src} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FASTCALL)
+    return FASTCALL
+
+
 def build(force: bool = False, verbose: bool = False, extra=(), debug_bounds: bool = False) -> str:
+    build_fastcall(force)
     lib, build_dir = (DEBUG_LIB, DEBUG_BUILD) if debug_bounds else (LIB, BUILD)
     if debug_bounds:
         extra = (*extra, "-DMTFM_DEBUG_BOUNDS")
