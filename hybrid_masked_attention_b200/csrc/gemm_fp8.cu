@@ -32,6 +32,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "gemm_fp8.cuh"
 #include "mma_util.cuh"
@@ -134,14 +135,16 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       : "memory");
 }
 
-// act, and the residual of a row whose 32 columns start at col.
-template <typename OT>
-__device__ __forceinline__ void finish32(const Args& p, int64_t orow, int col, float (&v)[32]) {
-  const Fp8Epi& e = p.epi;
-  if (e.act == MTFM_ACT_SILU) {
+__device__ __forceinline__ void act32(const Args& p, float (&v)[32]) {
+  if (p.epi.act == MTFM_ACT_SILU) {
 #pragma unroll
     for (int j = 0; j < 32; j += 2) silu2(v[j], v[j + 1]);
   }
+}
+// The residual of a row whose 32 columns start at col.
+template <typename OT>
+__device__ __forceinline__ void residual32(const Args& p, int64_t orow, int col, float (&v)[32]) {
+  const Fp8Epi& e = p.epi;
   if (!e.res) return;
   const int n = p.N - col;
   const OT* r = static_cast<const OT*>(e.res) + orow * e.ld_res + col;
@@ -232,9 +235,15 @@ __device__ __forceinline__ Tile tile_at(const Args& p, int t, int nM, int nN) {
   return {m * (2 * kBM), (b * p.n_group + in - m * w) * BN};
 }
 
-// TMA_OUT: the output leaves through 128-byte wide boxes staged in shared memory and TMA
-// stores (whole 16-byte aligned rows, one segment per map, no row map).
-template <int BN, typename OT, bool TMA_OUT>
+// How the output leaves a tile.
+//   kOutTma    : boxes of 128 rows x 128 bytes staged in shared memory, TMA stores; with a
+//                residual, which is then the fp32 output itself, TMA adds (one an element).
+//   kOutStaged : staged likewise; then each warp adds the residual to, and stores, whole 128-byte
+//                pieces of rows (with a residual or a row map: from the registers, where a thread
+//                has a row to itself, the same accesses touch 32 rows at a time and take twice as long).
+//   kOutDirect : rows that do not start, or whose end does not fall, on 16-byte boundaries.
+constexpr int kOutTma = 0, kOutStaged = 1, kOutDirect = 2;
+template <int BN, typename OT, int OUT>
 __global__ void __launch_bounds__(kThreadsG, 1)
 gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_o0, const __grid_constant__ CUtensorMap tm_o1,
@@ -422,6 +431,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     const uint32_t accf0 = b_accf + (uint32_t)((wg >> 1) * kAcc) * 8;            // BN = 256: by part; 128: by set
     const uint32_t acce0 = map_rank(b_acce + (uint32_t)(part * kAcc) * 8, 0);  // (mapped once: mapa in the loop cost 140 cycles a block)
     const bool issuer = quad == 0 && lane == 0;
+    const int tid = threadIdx.x & 127;
+    auto orow = [&](int m) { return (int64_t)(p.epi.row_map ? p.epi.row_map[m] : m); };
     bool ok = true;
     uint32_t n = (uint32_t)(set * nK);  // blocks before this set's next one: buffer n % kAcc
     uint32_t phases = 0;                // of this set's barriers, one bit a buffer
@@ -476,7 +487,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                                          acc[c * 16 + j]);
         }
       }
-      if (TMA_OUT) {
+      if (OUT != kOutDirect) {
         // uniform over the warpgroup before its barriers
         uint32_t all;
         asm volatile(
@@ -485,26 +496,29 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         ok = all != 0;
       }
       if (!ok) break;
-      const int64_t orow = row < p.M ? (p.epi.row_map ? p.epi.row_map[row] : row) : 0;
-      if constexpr (TMA_OUT) {
-        constexpr int kBoxCols = 128 / (int)sizeof(OT);  // 64 bf16 or 32 fp32
+      if constexpr (OUT != kOutDirect) {
+        using BT = typename std::conditional<OUT == kOutTma, OT, float>::type;  // staged before a residual: unrounded
+        constexpr int kBoxCols = 128 / (int)sizeof(BT);  // 64 bf16 or 32 fp32
+        uint8_t* rowp = stage + r_in * 128;
 #pragma unroll
         for (int b = 0; b < kCols / kBoxCols; ++b) {
-          if (issuer) bulk_wait_read<0>();  // the last store has read the staging
+          const int col = col0 + b * kBoxCols;
+          if constexpr (OUT == kOutTma) {
+            if (issuer) bulk_wait_read<0>();  // the last store has read the staging
+          }
           wg_sync(bar_id);
-          uint8_t* rowp = stage + r_in * 128;
 #pragma unroll
           for (int c = 0; c < kBoxCols / 32; ++c) {
-            const int col = b * kBoxCols + c * 32;  // within the warpgroup's columns
+            const int wc = b * kBoxCols + c * 32;  // within the warpgroup's columns
             float v[32];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[2 * j] = acc[col / 2 + j].x, v[2 * j + 1] = acc[col / 2 + j].y;
-            if (row < p.M && col0 + col < p.N) finish32<OT>(p, orow, col0 + col, v);
+            for (int j = 0; j < 16; ++j) v[2 * j] = acc[wc / 2 + j].x, v[2 * j + 1] = acc[wc / 2 + j].y;
+            act32(p, v);
 #pragma unroll
-            for (int i = 0; i < 2 * (int)sizeof(OT); ++i) {
-              const int chunk = c * 2 * (int)sizeof(OT) + i;
+            for (int i = 0; i < 2 * (int)sizeof(BT); ++i) {
+              const int chunk = c * 2 * (int)sizeof(BT) + i;
               uint4 w;
-              if constexpr (sizeof(OT) == 4)
+              if constexpr (sizeof(BT) == 4)
                 w = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
                                __float_as_uint(v[4 * i + 3]));
               else
@@ -513,20 +527,54 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
               *reinterpret_cast<uint4*>(rowp + ((chunk ^ (r_in & 7)) << 4)) = w;
             }
           }
-          fence_proxy_async();
-          wg_sync(bar_id);
-          const int col = col0 + b * kBoxCols;
-          if (issuer && m0 < p.M && col < p.N) {
-            const CUtensorMap* om = &tm_o0;
-            int begin = 0;
+          if constexpr (OUT == kOutTma) {
+            fence_proxy_async();
+            wg_sync(bar_id);
+            if (issuer && m0 < p.M && col < p.N) {
+              const CUtensorMap* om = &tm_o0;
+              int begin = 0;
 #pragma unroll
-            for (int q = 1; q < 4; ++q)
-              if (q < p.epi.n_seg && col >= p.epi.seg_begin[q]) {
-                begin = p.epi.seg_begin[q];
-                om = q == 1 ? &tm_o1 : q == 2 ? &tm_o2 : &tm_o3;
+              for (int q = 1; q < 4; ++q)
+                if (q < p.epi.n_seg && col >= p.epi.seg_begin[q]) {
+                  begin = p.epi.seg_begin[q];
+                  om = q == 1 ? &tm_o1 : q == 2 ? &tm_o2 : &tm_o3;
+                }
+              if (p.epi.res) tma_reduce_add_2d(om, sstage, col - begin, m0);
+              else tma_store_2d(om, sstage, col - begin, m0);
+              bulk_commit();
+            }
+          } else {
+            // piece i of this thread: 4 columns of row 16 i + tid / 8; four pieces at a time, loaded once
+            // the box's sums have left their registers
+            wg_sync(bar_id);
+#pragma unroll 1
+            for (int i0 = 0; i0 < 8; i0 += 4) {
+              const int r0 = 16 * i0 + (tid >> 3), c = col + (tid & 7) * 4;
+              Raw<OT> res[4];
+              if (p.epi.res) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int m = m0 + r0 + 16 * i;
+                  if (m < p.M && c < p.N)
+                    res[i] = load_raw<true>(static_cast<const OT*>(p.epi.res) + orow(m) * p.epi.ld_res + c, 0, 4);
+                }
               }
-            tma_store_2d(om, sstage, col - begin, m0);
-            bulk_commit();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = r0 + 16 * i, m = m0 + r;
+                const float4 w = *reinterpret_cast<const float4*>(stage + r * 128 + (((tid & 7) ^ (r & 7)) << 4));
+                float v[4] = {w.x, w.y, w.z, w.w};
+                if (m < p.M && c < p.N) {
+                  if (p.epi.res) {
+                    float t[4];
+                    unpack(res[i], t);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] += t[j];
+                  }
+                  put4<true>(static_cast<OT*>(p.epi.seg_ptr[0]) + orow(m) * p.epi.seg_ld[0] + c, 0, 4, v);
+                }
+              }
+            }
           }
         }
       } else if (row < p.M) {
@@ -536,13 +584,14 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             float v[32];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[2 * j] = acc[c * 16 + j].x, v[2 * j + 1] = acc[c * 16 + j].y;
-            finish32<OT>(p, orow, col0 + c * 32, v);
-            store32<OT>(p, orow, col0 + c * 32, v);
+            act32(p, v);
+            residual32<OT>(p, orow(row), col0 + c * 32, v);
+            store32<OT>(p, orow(row), col0 + c * 32, v);
           }
         }
       }
     }
-    if (TMA_OUT && issuer) bulk_wait<0>();  // every store has completed before the CTA leaves
+    if (OUT == kOutTma && issuer) bulk_wait<0>();  // every store has completed before the CTA leaves
   }
   pdl_trigger();
   __syncthreads();
@@ -568,10 +617,10 @@ bool make_map_out(CUtensorMap* map, void* base, int type, int rows, int cols, in
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, typename OT, bool TMA_OUT>
+template <int BN, typename OT, int OUT>
 cudaError_t go(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap (&mo)[4], const Args& args, int64_t tiles,
                cudaStream_t st) {
-  auto kern = gemm_fp8_kernel<BN, OT, TMA_OUT>;
+  auto kern = gemm_fp8_kernel<BN, OT, OUT>;
   const size_t smem = smem_g<BN>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -599,17 +648,26 @@ cudaError_t launch(const Fp8In& a, const Fp8In& b, Args& args, cudaStream_t st) 
     return cudaErrorInvalidValue;
   const Fp8Epi& e = args.epi;
   const int box_cols = 128 / dtype_size(e.out_type);
-  bool tma = args.vec && !e.row_map;
   // a TMA store writes whole 16-byte pieces of a row: a row that ends inside one is stored directly
-  for (int s = 0; s < e.n_seg && tma; ++s)
-    tma = e.seg_begin[s] % box_cols == 0 && (e.seg_begin[s + 1] - e.seg_begin[s]) * dtype_size(e.out_type) % 16 == 0 &&
-          make_map_out(&mo[s], e.seg_ptr[s], e.out_type, args.M, e.seg_begin[s + 1] - e.seg_begin[s], e.seg_ld[s]);
+  bool whole = args.vec;
+  for (int s = 0; s < e.n_seg; ++s)
+    whole = whole && (e.seg_begin[s + 1] - e.seg_begin[s]) * dtype_size(e.out_type) % 16 == 0;
+  const bool onto_out = e.res == e.seg_ptr[0] && e.ld_res == e.seg_ld[0] && e.out_type == MTFM_F32;
+  int out = !whole ? kOutDirect : (e.res && !onto_out) || e.row_map ? kOutStaged : kOutTma;
+  if (out == kOutStaged && e.n_seg > 1) out = kOutDirect;
+  for (int s = 0; s < e.n_seg && out == kOutTma; ++s)
+    if (e.seg_begin[s] % box_cols != 0 ||
+        !make_map_out(&mo[s], e.seg_ptr[s], e.out_type, args.M, e.seg_begin[s + 1] - e.seg_begin[s], e.seg_ld[s]))
+      out = kOutDirect;
   const int64_t nM = ((int64_t)args.M + 2 * kBM - 1) / (2 * kBM), nN = ((int64_t)args.N + BN - 1) / BN;
   args.n_group = (int)std::min<int64_t>(nN, 8);
-  if (e.out_type == MTFM_BF16)
-    return tma ? go<BN, __nv_bfloat16, true>(ma, mb, mo, args, nM * nN, st)
-               : go<BN, __nv_bfloat16, false>(ma, mb, mo, args, nM * nN, st);
-  return tma ? go<BN, float, true>(ma, mb, mo, args, nM * nN, st) : go<BN, float, false>(ma, mb, mo, args, nM * nN, st);
+  auto by_out = [&](auto type) {
+    using OT = decltype(type);
+    return out == kOutTma      ? go<BN, OT, kOutTma>(ma, mb, mo, args, nM * nN, st)
+           : out == kOutStaged ? go<BN, OT, kOutStaged>(ma, mb, mo, args, nM * nN, st)
+                               : go<BN, OT, kOutDirect>(ma, mb, mo, args, nM * nN, st);
+  };
+  return e.out_type == MTFM_BF16 ? by_out(__nv_bfloat16{}) : by_out(float{});
 }
 
 }  // namespace
@@ -625,8 +683,13 @@ cudaError_t launch_gemm_fp8(int32_t* err, int M, int N, int K, const Fp8In& a, c
   bool vec = !epi.res || rows16(epi.res, epi.ld_res);
   for (int s = 0; s < epi.n_seg; ++s) vec = vec && rows16(epi.seg_ptr[s], epi.seg_ld[s]);
   Args args{err, M, N, K, a.scale, a.ld_scale, b.scale, b.ld_scale, epi, 1, vec};
-  const int64_t tiles256 = (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256);
-  return tiles256 >= sm_count() / 2 ? launch<256>(a, b, args, st) : launch<128>(a, b, args, st);
+  // Tile width by the rounds the pairs make: a round of 256 x 128 tiles takes 0.55 (short K) to
+  // 0.62 (long K) of one of 256 x 256 (8192^3 forced to 128 columns: 647 against 520 us; 4911 x
+  // 1000 x 1000, 3 rounds against 2: 17 and 19).
+  const int64_t pairs = sm_count() / 2, nM = ((int64_t)M + 255) / 256;
+  const int64_t r256 = (nM * (((int64_t)N + 255) / 256) + pairs - 1) / pairs;
+  const int64_t r128 = (nM * (((int64_t)N + 127) / 128) + pairs - 1) / pairs;
+  return 10 * r256 <= 6 * r128 ? launch<256>(a, b, args, st) : launch<128>(a, b, args, st);
 }
 
 }  // namespace mtfm
