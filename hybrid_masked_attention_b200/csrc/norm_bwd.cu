@@ -43,12 +43,13 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
   constexpr int kWarps = kThreadsB<C> / 32;
   using RRaw = typename std::conditional<kRes, RT, XT>::type;
   extern __shared__ float s_dw[];  // [rows of a block - 1][dim]
-  __shared__ float s_part[2][kWarps];
+  __shared__ __align__(16) float s_part[2][kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int W = p.W, sub = warp % W, slot = warp / W, R = kWarps / W;
   const int G = (p.dim + kGroup - 1) / kGroup;
   pdl_wait();
   pdl_trigger();
+  const float inv_dim = 1.f / (float)p.dim;
   float dw[C][4];
 #pragma unroll
   for (int i = 0; i < C; ++i)
@@ -107,11 +108,10 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
     if (W > 1) {
       if (lane == 0) s_part[flip][warp] = s;
       __syncthreads();
-      s = 0.f;
-      for (int k = 0; k < W; ++k) s += s_part[flip][warp - sub + k];
+      s = row_sum(s_part[flip] + warp - sub, W);
     }
     if (live) {
-      const float c = s / (float)p.dim * r * r;
+      const float c = s * inv_dim * r * r;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const int g = i * W + sub;

@@ -48,7 +48,7 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
   constexpr bool kDelta = !std::is_same<DT, None>::value;
   using DRaw = typename std::conditional<kDelta, DT, XT>::type;
   constexpr int kWarps = kThreadsN<C, MULTI> / 32;
-  __shared__ float s_part[2][kWarps];
+  __shared__ __align__(16) float s_part[2][kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int W = MULTI ? p.W : 1;
   const int sub = MULTI ? warp % W : 0, slot = MULTI ? warp / W : warp;
@@ -103,8 +103,7 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
     if (MULTI) {
       if (lane == 0) s_part[flip][warp] = s;
       __syncthreads();
-      s = 0.f;
-      for (int k = 0; k < W; ++k) s += s_part[flip][warp - sub + k];
+      s = row_sum(s_part[flip] + warp - sub, W);
     }
     if (row >= p.rows) continue;
     const float r = 1.f / sqrtf(s / (float)p.dim + p.eps);

@@ -18,7 +18,7 @@ quant_rows_kernel(int rows, int cols, int parts, int step_rows, int step_parts, 
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t unit = (int64_t)blockIdx.x * 8 + warp_index();
   int64_t row = unit / parts;
   int part = (int)(unit % parts);
   Raw<T> next[kPer];
@@ -61,7 +61,7 @@ quant_blocks_kernel(int rows, int cols, int G, const T* __restrict__ x, int64_t 
   __shared__ float s_max[8];
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int rb = blockIdx.x / G, g = blockIdx.x % G;
   const int64_t r0 = (int64_t)rb * kGroup;
   const int c0 = g * kGroup, n = cols - c0;
