@@ -21,7 +21,7 @@
 //
 // Warp 0 issues TMA; warps 1 and 3 of the leading CTA issue the MMAs of the pair (one warp for
 // both halves kept the tensor pipe waiting: 412 against 311 us at 8192^3 with nothing else in
-// the way); warp 2 brings the A scales, 128 rows a block, to shared memory (read from global
+// the way); warp 2 brings the scales, 128 rows of A a block, to shared memory (read from global
 // memory by the epilogue warps themselves, 32 rows a warp and each row in 4 warpgroups, they
 // cost 100 us of 560); warps 4..19 are the warpgroups, one TMEM lane (row) a thread.  Their 64
 // sums a thread take registers that the first four warps hand over (setmaxnreg).
@@ -87,6 +87,7 @@ struct Bars {
   uint64_t acc_full[8], acc_empty[4];   // TMEM buffers (acc_full: per part, or per set)
   uint64_t sc_full[2 * kSlots], sc_empty[kSlots];  // scales (sc_full: per set)
   uint64_t drain[2];
+  float sb[kSlots][2];                  // B scales of a block, one for each 128 columns of the tile
   uint32_t tmem, skip;
   int abort;
 };
@@ -387,14 +388,17 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         }
       }
     } else if (warp == 2) {
-      // ----------------------------------------------------------- A scales (each CTA): lane l
-      // copies rows l, l + 32, l + 64, l + 96 of a block; rows past M become 0
+      // ----------------------------------------------------------- scales (each CTA): lane l copies
+      // those of rows l, l + 32, l + 64, l + 96 of a block; rows past M become 0
       bool ok = true;
       int slot = 0, set = 0;
       uint32_t ph = 0;
       for (int t = first; ok && t < n_tiles; t += step, set ^= 1) {
-        const int row = tile_at<BN>(p, t, nM, nN).m0 + (int)rank * kBM + lane;
+        const Tile tl = tile_at<BN>(p, t, nM, nN);
+        const int row = tl.m0 + (int)rank * kBM + lane;
         const float* src = p.sa + (int64_t)row * p.ld_sa;
+        const int bcol = tl.n0 + lane * 128;  // of lanes 0 .. kParts - 1: columns past N have no scale
+        const float* src_b = p.sb + (int64_t)((bcol < p.N ? bcol : p.N - 1) / kGroup) * p.ld_sb;
         for (int kb = 0; kb < nK; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(b_sce + slot * 8, ph ^ 1, abort_flag))) {
             ok = false;
@@ -406,6 +410,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             const bool in = row + 32 * i < p.M;
             copy4(dst + i * 128, in ? src + (int64_t)(32 * i) * p.ld_sa + kb : p.sa, in ? 4 : 0);
           }
+          if (lane < kParts) copy4(smem_addr(&bars.sb[slot][lane]), src_b + kb, 4);
           copy_arrive(b_scf + (uint32_t)((kParts > 1 ? 0 : set) * kSlots + slot) * 8);
           if (++slot == kSlots) {
             slot = 0;
@@ -440,28 +445,34 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     const volatile float* s_scale = reinterpret_cast<const volatile float*>(smem + scale_off<BN>());
     int slot = set * nK % kSlots;
     uint32_t sc_phases = 0;
+    float sc = 0.f;  // sa sb of this thread's row and columns for the next block
+    auto next_scale = [&]() {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(scf0 + (uint32_t)slot * 8, (sc_phases >> slot) & 1, abort_flag));
+      sc = s_scale[slot * 128 + r_in] * *const_cast<const volatile float*>(&bars.sb[slot][part]);
+      sc_phases ^= 1u << slot;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_sce + (uint32_t)slot * 8);
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
+      return got;
+    };
+    // BN = 256: a tile's first scale is fetched in the last block of the one before.  With sets it
+    // is fetched when the tile begins: a set that waited for it while it holds a TMEM buffer would
+    // wait for the other set's tile, which needs that buffer.
+    if (kSets == 1 && first < n_tiles) ok = next_scale();
     for (int t = first + set * step; ok && t < n_tiles; t += kSets * step, n += (uint32_t)((kSets - 1) * nK), slot = (slot + (kSets - 1) * nK) % kSlots) {
       const Tile tl = tile_at<BN>(p, t, nM, nN);
       const int m0 = tl.m0 + (int)rank * kBM;
       const int row = m0 + r_in;
       const int col0 = tl.n0 + tcol;
-      // the warpgroup's columns lie in one 128-row block of B; columns past N have no scale of their own
-      const float* sb = p.sb + (int64_t)((col0 < p.N ? col0 : p.N - 1) / kGroup) * p.ld_sb;
       float2 acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-      float sb_next = sb[0];
+      if (kSets > 1) {
+        ok = next_scale();
+        if (!ok) break;
+      }
       for (int kb = 0; kb < nK; ++kb, ++n) {
-        if (!__all_sync(0xffffffffu, mbar_wait(scf0 + (uint32_t)slot * 8, (sc_phases >> slot) & 1, abort_flag))) {
-          ok = false;
-          break;
-        }
-        const float sc = s_scale[slot * 128 + r_in] * sb_next;
-        if (kb + 1 < nK) sb_next = sb[kb + 1];
-        sc_phases ^= 1u << slot;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b_sce + (uint32_t)slot * 8);
-        slot = slot + 1 == kSlots ? 0 : slot + 1;
+        const float2 s2 = make_float2(sc, sc);
         const int a = (int)(n % kAcc);
         if (!__all_sync(0xffffffffu, mbar_wait(accf0 + (uint32_t)a * 8, (phases >> a) & 1, abort_flag))) {
           ok = false;
@@ -470,11 +481,13 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         phases ^= 1u << a;
         tc_fence_after();
         const uint32_t ta = tlane + (uint32_t)(a * 128);
-        const float2 s2 = make_float2(sc, sc);
 #pragma unroll
         for (int c = 0; c < kCols / 32; ++c) {
           uint32_t raw[32];
           tmem_ld32(ta + (uint32_t)(c * 32), raw);
+          if (c == 0) {  // the next block's scale is fetched while this one is on its way from TMEM
+            if (kb + 1 < nK || (kSets == 1 && t + step < n_tiles)) ok = next_scale();
+          }
           tmem_ld_wait();
           if (c + 1 == kCols / 32) {
             tc_fence_before();
