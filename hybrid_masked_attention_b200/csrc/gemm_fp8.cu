@@ -65,8 +65,19 @@ struct Args {
 
 template <int BN>
 constexpr uint32_t stage_bytes_g() { return kABytes + (uint32_t)(BN / 2) * kGroup; }
-template <int BN>
-constexpr int stages_g() { return BN == 256 ? 5 : 6; }
+// How the output leaves a tile.
+//   kOutTma    : boxes of 128 rows x 128 bytes staged in shared memory, TMA stores.
+//   kOutTmaRes : the same with a residual, whose boxes TMA brings into the staging while the tile
+//                is computed (BN = 128: the second fp32 box of a warpgroup takes two ring stages).
+//   kOutStaged : with a row map: staged, then each warp adds the residual to, and stores, whole
+//                128-byte pieces of rows (a thread's own row, from its registers, would touch 32
+//                rows at a time: 4911 x 1000 x 1000 took 40 us that way and 23 this way).
+//   kOutDirect : rows that do not start, or whose end does not fall, on 16-byte boundaries.
+constexpr int kOutTma = 0, kOutStaged = 1, kOutDirect = 2, kOutTmaRes = 3;
+template <int BN, int OUT>
+constexpr int stages_g() { return BN == 256 ? 5 : OUT == kOutTmaRes ? 4 : 6; }
+template <int OUT>
+constexpr int boxes_g() { return OUT == kOutTmaRes ? 2 : 1; }  // staged boxes of a warpgroup
 // Parts of a tile with their own MMAs, and TMEM buffers of a part (512 columns in all).
 template <int BN>
 constexpr int parts_g() { return BN / 128; }
@@ -74,24 +85,26 @@ template <int BN>
 constexpr int acc_bufs() { return 512 / BN; }
 constexpr int kSlots = 5;  // blocks of A scales in shared memory
 // Dynamic shared memory (there is no static): the ring, the staged boxes, the scales, barriers.
-template <int BN>
-constexpr uint32_t stage_off() { return stages_g<BN>() * stage_bytes_g<BN>(); }
-template <int BN>
-constexpr uint32_t scale_off() { return stage_off<BN>() + kGroupsWG * kBoxBytes; }
-template <int BN>
-constexpr uint32_t bars_off() { return scale_off<BN>() + kSlots * 128 * 4; }
-template <int BN>
-constexpr size_t smem_g() { return bars_off<BN>() + 512; }
+template <int BN, int OUT>
+constexpr uint32_t stage_off() { return stages_g<BN, OUT>() * stage_bytes_g<BN>(); }
+template <int BN, int OUT>
+constexpr uint32_t scale_off() { return stage_off<BN, OUT>() + kGroupsWG * boxes_g<OUT>() * kBoxBytes; }
+template <int BN, int OUT>
+constexpr uint32_t bars_off() { return scale_off<BN, OUT>() + kSlots * 128 * 4; }
+template <int BN, int OUT>
+constexpr size_t smem_g() { return bars_off<BN, OUT>() + 512; }
 struct Bars {
   uint64_t full[6], empty[6];           // ring stages
   uint64_t acc_full[8], acc_empty[4];   // TMEM buffers (acc_full: per part, or per set)
   uint64_t sc_full[2 * kSlots], sc_empty[kSlots];  // scales (sc_full: per set)
+  uint64_t res_full[kGroupsWG];  // a warpgroup's residual boxes have landed
   uint64_t drain[2];
   float sb[kSlots][2];                  // B scales of a block, one for each 128 columns of the tile
   uint32_t tmem, skip;
   int abort;
 };
-static_assert(sizeof(Bars) <= 512 && smem_g<256>() <= 232448, "shared memory of an SM");
+static_assert(sizeof(Bars) <= 512 && smem_g<256, kOutTma>() <= 232448 && smem_g<128, kOutTmaRes>() <= 232448,
+              "shared memory of an SM");
 
 // ---------------------------------------------------------------- CTA pairs
 // Relaxed: what it hands over is TMEM that this warp has finished reading (tcgen05.wait::ld and
@@ -236,25 +249,17 @@ __device__ __forceinline__ Tile tile_at(const Args& p, int t, int nM, int nN) {
   return {m * (2 * kBM), (b * p.n_group + in - m * w) * BN};
 }
 
-// How the output leaves a tile.
-//   kOutTma    : boxes of 128 rows x 128 bytes staged in shared memory, TMA stores; with a
-//                residual, which is then the fp32 output itself, TMA adds (one an element).
-//   kOutStaged : staged likewise; then each warp adds the residual to, and stores, whole 128-byte
-//                pieces of rows (with a residual or a row map: from the registers, where a thread
-//                has a row to itself, the same accesses touch 32 rows at a time and take twice as long).
-//   kOutDirect : rows that do not start, or whose end does not fall, on 16-byte boundaries.
-constexpr int kOutTma = 0, kOutStaged = 1, kOutDirect = 2;
 template <int BN, typename OT, int OUT>
 __global__ void __launch_bounds__(kThreadsG, 1)
 gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_o0, const __grid_constant__ CUtensorMap tm_o1,
                 const __grid_constant__ CUtensorMap tm_o2, const __grid_constant__ CUtensorMap tm_o3,
                 const __grid_constant__ Args p) {
-  constexpr int kStages = stages_g<BN>(), kParts = parts_g<BN>(), kAcc = acc_bufs<BN>();
+  constexpr int kStages = stages_g<BN, OUT>(), kParts = parts_g<BN>(), kAcc = acc_bufs<BN>();
   constexpr uint32_t kStage = stage_bytes_g<BN>();
   constexpr uint32_t kTmemCols = 512;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Bars& bars = *reinterpret_cast<Bars*>(smem + bars_off<BN>());
+  Bars& bars = *reinterpret_cast<Bars*>(smem + bars_off<BN, OUT>());
 
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -277,6 +282,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     for (int a = 0; a < kParts * kAcc; ++a) mbar_init(b_acce + a * 8, 16);  // two warpgroups of both CTAs
     for (int a = 0; a < 2 * kSlots; ++a) mbar_init(b_scf + a * 8, 32);      // the lanes of warp 2
     for (int a = 0; a < kSlots; ++a) mbar_init(b_sce + a * 8, 8 * kParts);  // the warps of the tile's set
+    for (int a = 0; a < kGroupsWG; ++a) mbar_init(smem_addr(&bars.res_full[a]), 1);
     mbar_init(smem_addr(&bars.drain[0]), 1);
     mbar_init(smem_addr(&bars.drain[1]), 1);
     fence_barrier_init();
@@ -404,7 +410,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             ok = false;
             break;
           }
-          const uint32_t dst = sbase + scale_off<BN>() + (uint32_t)(slot * 128 + lane) * 4;
+          const uint32_t dst = sbase + scale_off<BN, OUT>() + (uint32_t)(slot * 128 + lane) * 4;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const bool in = row + 32 * i < p.M;
@@ -430,19 +436,24 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     const int part = kParts > 1 ? wg >> 1 : 0;
     const int tcol = kSets > 1 ? (wg & 1) * kCols : wg * kCols;  // first column within the tile
     const uint32_t tlane = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(part * (kAcc * 128) + (wg & 1) * kCols);
-    uint8_t* stage = smem + stage_off<BN>() + wg * kBoxBytes;
+    uint8_t* stage = smem + stage_off<BN, OUT>() + wg * (boxes_g<OUT>() * kBoxBytes);
     const uint32_t sstage = smem_addr(stage);
     const int bar_id = 2 + wg;
     const uint32_t accf0 = b_accf + (uint32_t)((wg >> 1) * kAcc) * 8;            // BN = 256: by part; 128: by set
     const uint32_t acce0 = map_rank(b_acce + (uint32_t)(part * kAcc) * 8, 0);  // (mapped once: mapa in the loop cost 140 cycles a block)
     const bool issuer = quad == 0 && lane == 0;
     const int tid = threadIdx.x & 127;
+    constexpr int kOutCols = 128 / (int)sizeof(OT);       // columns of a box of the output's type
+    constexpr int kResBoxes = kCols / kOutCols;
+    constexpr uint32_t kResBytes = kResBoxes * kBoxBytes;
+    const uint32_t b_res = smem_addr(&bars.res_full[wg]);
+    uint32_t res_issued = 0, ph_res = 0;
     auto orow = [&](int m) { return (int64_t)(p.epi.row_map ? p.epi.row_map[m] : m); };
     bool ok = true;
     uint32_t n = (uint32_t)(set * nK);  // blocks before this set's next one: buffer n % kAcc
     uint32_t phases = 0;                // of this set's barriers, one bit a buffer
     const uint32_t scf0 = b_scf + (uint32_t)((kParts > 1 ? 0 : set) * kSlots) * 8;
-    const volatile float* s_scale = reinterpret_cast<const volatile float*>(smem + scale_off<BN>());
+    const volatile float* s_scale = reinterpret_cast<const volatile float*>(smem + scale_off<BN, OUT>());
     int slot = set * nK % kSlots;
     uint32_t sc_phases = 0;
     float sc = 0.f;  // sa sb of this thread's row and columns for the next block
@@ -464,6 +475,13 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       const int m0 = tl.m0 + (int)rank * kBM;
       const int row = m0 + r_in;
       const int col0 = tl.n0 + tcol;
+      if (OUT == kOutTmaRes && issuer) {
+        bulk_wait_read<0>();  // the last tile's stores have read the staging
+        mbar_expect_tx(b_res, kResBytes);
+#pragma unroll
+        for (int b = 0; b < kResBoxes; ++b) tma_load_2d(sstage + b * kBoxBytes, &tm_o1, b_res, col0 + b * kOutCols, m0);
+        ++res_issued;
+      }
       float2 acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
@@ -509,7 +527,50 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         ok = all != 0;
       }
       if (!ok) break;
-      if constexpr (OUT != kOutDirect) {
+      if constexpr (OUT == kOutTmaRes) {
+        // (a wait that gives up leaves the warpgroup's barriers below whole: every warp goes on)
+        ok = mbar_wait(b_res, ph_res, abort_flag);
+        ph_res ^= 1;
+#pragma unroll
+        for (int b = 0; b < kResBoxes; ++b) {
+          uint8_t* rowp = stage + b * kBoxBytes + r_in * 128;
+#pragma unroll
+          for (int c = 0; c < kOutCols / 32; ++c) {
+            const int wc = b * kOutCols + c * 32;  // within the warpgroup's columns
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[2 * j] = acc[wc / 2 + j].x, v[2 * j + 1] = acc[wc / 2 + j].y;
+            act32(p, v);
+#pragma unroll
+            for (int i = 0; i < 2 * (int)sizeof(OT); ++i) {
+              uint4* at = reinterpret_cast<uint4*>(rowp + (((c * 2 * (int)sizeof(OT) + i) ^ (r_in & 7)) << 4));
+              uint4 w = *at;
+              if constexpr (sizeof(OT) == 4) {
+                w.x = __float_as_uint(v[4 * i] + __uint_as_float(w.x));
+                w.y = __float_as_uint(v[4 * i + 1] + __uint_as_float(w.y));
+                w.z = __float_as_uint(v[4 * i + 2] + __uint_as_float(w.z));
+                w.w = __float_as_uint(v[4 * i + 3] + __uint_as_float(w.w));
+              } else {
+                auto sum = [&](uint32_t r, int j) {
+                  return pack_bf16x2(v[8 * i + j] + __uint_as_float(r << 16),
+                                     v[8 * i + j + 1] + __uint_as_float(r & 0xffff0000u));
+                };
+                w = make_uint4(sum(w.x, 0), sum(w.y, 2), sum(w.z, 4), sum(w.w, 6));
+              }
+              *at = w;
+            }
+          }
+        }
+        fence_proxy_async();
+        wg_sync(bar_id);
+        if (issuer && ok && m0 < p.M) {
+#pragma unroll
+          for (int b = 0; b < kResBoxes; ++b)
+            if (col0 + b * kOutCols < p.N) tma_store_2d(&tm_o0, sstage + b * kBoxBytes, col0 + b * kOutCols, m0);
+          bulk_commit();
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      } else if constexpr (OUT != kOutDirect) {
         using BT = typename std::conditional<OUT == kOutTma, OT, float>::type;  // staged before a residual: unrounded
         constexpr int kBoxCols = 128 / (int)sizeof(BT);  // 64 bf16 or 32 fp32
         uint8_t* rowp = stage + r_in * 128;
@@ -552,8 +613,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                   begin = p.epi.seg_begin[q];
                   om = q == 1 ? &tm_o1 : q == 2 ? &tm_o2 : &tm_o3;
                 }
-              if (p.epi.res) tma_reduce_add_2d(om, sstage, col - begin, m0);
-              else tma_store_2d(om, sstage, col - begin, m0);
+              tma_store_2d(om, sstage, col - begin, m0);
               bulk_commit();
             }
           } else {
@@ -604,7 +664,13 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         }
       }
     }
-    if (OUT == kOutTma && issuer) bulk_wait<0>();  // every store has completed before the CTA leaves
+    if (issuer) {
+      if (OUT == kOutTma || OUT == kOutTmaRes) bulk_wait<0>();  // every store has completed before the CTA leaves
+      // and no copy may land after it: after a wait that gave up, the residual's boxes may be on their way
+      const long long t0 = clock64();
+      while (OUT == kOutTmaRes && res_issued > 0 && !mbar_try(b_res, (res_issued - 1) & 1) && clock64() - t0 < kWaitCycles) {
+      }
+    }
   }
   pdl_trigger();
   __syncthreads();
@@ -634,7 +700,7 @@ template <int BN, typename OT, int OUT>
 cudaError_t go(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap (&mo)[4], const Args& args, int64_t tiles,
                cudaStream_t st) {
   auto kern = gemm_fp8_kernel<BN, OT, OUT>;
-  const size_t smem = smem_g<BN>();
+  const size_t smem = smem_g<BN, OUT>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
@@ -665,18 +731,20 @@ cudaError_t launch(const Fp8In& a, const Fp8In& b, Args& args, cudaStream_t st) 
   bool whole = args.vec;
   for (int s = 0; s < e.n_seg; ++s)
     whole = whole && (e.seg_begin[s + 1] - e.seg_begin[s]) * dtype_size(e.out_type) % 16 == 0;
-  const bool onto_out = e.res == e.seg_ptr[0] && e.ld_res == e.seg_ld[0] && e.out_type == MTFM_F32;
-  int out = !whole ? kOutDirect : (e.res && !onto_out) || e.row_map ? kOutStaged : kOutTma;
+  int out = !whole ? kOutDirect : e.row_map ? kOutStaged : e.res ? kOutTmaRes : kOutTma;
   if (out == kOutStaged && e.n_seg > 1) out = kOutDirect;
-  for (int s = 0; s < e.n_seg && out == kOutTma; ++s)
+  for (int s = 0; s < e.n_seg && (out == kOutTma || out == kOutTmaRes); ++s)
     if (e.seg_begin[s] % box_cols != 0 ||
         !make_map_out(&mo[s], e.seg_ptr[s], e.out_type, args.M, e.seg_begin[s + 1] - e.seg_begin[s], e.seg_ld[s]))
       out = kOutDirect;
+  if (out == kOutTmaRes && !make_map_out(&mo[1], const_cast<void*>(e.res), e.out_type, args.M, args.N, e.ld_res)) out = kOutDirect;
+  if (out == kOutTmaRes && BN == 256) return launch<128>(a, b, args, st);
   const int64_t nM = ((int64_t)args.M + 2 * kBM - 1) / (2 * kBM), nN = ((int64_t)args.N + BN - 1) / BN;
   args.n_group = (int)std::min<int64_t>(nN, 8);
   auto by_out = [&](auto type) {
     using OT = decltype(type);
     return out == kOutTma      ? go<BN, OT, kOutTma>(ma, mb, mo, args, nM * nN, st)
+           : out == kOutTmaRes ? go<128, OT, kOutTmaRes>(ma, mb, mo, args, nM * nN, st)
            : out == kOutStaged ? go<BN, OT, kOutStaged>(ma, mb, mo, args, nM * nN, st)
                                : go<BN, OT, kOutDirect>(ma, mb, mo, args, nM * nN, st);
   };
