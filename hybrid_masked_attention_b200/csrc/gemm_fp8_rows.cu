@@ -268,7 +268,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
       auto finish = [&](int m, float v) {
         if (e.act == MTFM_ACT_SILU) {
           float other = 0.f;
-          silu2(v, other);
+          silu_pair<OT>(v, other);
         }
         const int64_t orow = e.row_map ? e.row_map[m] : m;
         if (e.res) v += (float)static_cast<const OT*>(e.res)[orow * e.ld_res + col];
