@@ -364,17 +364,15 @@ mtfm_status stack_fwd(const mtfm_cfg* cfg, const void* d_meta, int d, int n_laye
 // Scratch of one layer with 8-bit projections: as StackWs, with X~, X~_T and Y as e4m3 and
 // their scales (one for each 128 columns of a row).
 struct Fp8StackWs {
-  size_t xn, xn_s, xnt, xnt_s, u, q, k, v, a, y, y_s, stats, total;
+  size_t xn, xn_s, u, q, k, v, a, y, y_s, stats, total;
 };
 Fp8StackWs fp8_stack_ws(const Resolved& r, int d) {
   Fp8StackWs w;
   const size_t N = (size_t)r.total_tokens, T = (size_t)r.total_t;
   const size_t gd = (d + kGroup - 1) / kGroup, gD = (r.D + kGroup - 1) / kGroup;
   size_t o = 0;
-  w.xn = o;    o = align256(o + N * d);
-  w.xn_s = o;  o = align256(o + N * gd * 4);
-  w.xnt = o;   o = align256(o + T * d);
-  w.xnt_s = o; o = align256(o + T * gd * 4);
+  w.xn = o;    o = align256(o + (N + T) * d);  // X~, then X~_T
+  w.xn_s = o;  o = align256(o + (N + T) * gd * 4);
   w.u = o;     o = align256(o + N * r.D * 2);
   w.q = o;     o = align256(o + N * r.D * 2);
   w.k = o;     o = align256(o + N * r.Dkv * 2);
@@ -421,24 +419,23 @@ cudaError_t fp8_layer_fwd(const Resolved& r, const MetaView& m, const MetaLayout
   const MatIn xin{x, d, MTFM_F32}, none{nullptr, 0, MTFM_F32};
   const MatOut no_out{nullptr, 0, MTFM_F32};
   cudaError_t e;
-  // X~ of every row (K, V read all rows), and gathered for a Target layer's T rows
-  if ((e = launch_add_rmsnorm_fp8(err, N, d, xin, none, nullptr, w.rms_w, kRmsEps, no_out, out8(W.xn, W.xn_s, d), nullptr,
-                                  st)) != cudaSuccess)
+  // X~ of every row (K, V read all rows); for a Target layer, in the same launch, gathered T rows after them
+  if ((e = launch_add_rmsnorm_fp8(err, target ? N + T : N, d, xin, none, N, target ? m.t_rows : nullptr, w.rms_w, kRmsEps, no_out,
+                                  out8(W.xn, W.xn_s, d), nullptr, st)) != cudaSuccess)
     return e;
-  if (target && (e = launch_add_rmsnorm_fp8(err, T, d, xin, none, m.t_rows, w.rms_w, kRmsEps, no_out,
-                                            out8(W.xnt, W.xnt_s, d), nullptr, st)) != cudaSuccess)
-    return e;
+  const Fp8In xn = in8(W.xn, W.xn_s, d);
+  const Fp8In xnt{xn.q + (size_t)N * xn.ld, xn.ld, xn.scale + (size_t)N * xn.ld_scale, xn.ld_scale};
   if (!target) {
     const Fp8Epi g{MTFM_ACT_SILU, MTFM_BF16, 4, {0, D, 2 * D, 2 * D + Dkv, 2 * D + 2 * Dkv},
                    {bf(W.u), bf(W.q), bf(W.k), bf(W.v)}, {D, D, Dkv, Dkv}, nullptr, 0, nullptr};
-    if ((e = launch_gemm_fp8(err, N, 2 * D + 2 * Dkv, d, in8(W.xn, W.xn_s, d), wt(w.w_in), g, st)) != cudaSuccess) return e;
+    if ((e = launch_gemm_fp8(err, N, 2 * D + 2 * Dkv, d, xn, wt(w.w_in), g, st)) != cudaSuccess) return e;
   } else {
     const Fp8Epi guq{MTFM_ACT_SILU, MTFM_BF16, 2, {0, D, 2 * D, 2 * D, 2 * D}, {bf(W.u), bf(W.q), nullptr, nullptr},
                      {D, D, 0, 0}, nullptr, 0, nullptr};
-    if ((e = launch_gemm_fp8(err, T, 2 * D, d, in8(W.xnt, W.xnt_s, d), wt(w.w_in), guq, st)) != cudaSuccess) return e;
+    if ((e = launch_gemm_fp8(err, T, 2 * D, d, xnt, wt(w.w_in), guq, st)) != cudaSuccess) return e;
     const Fp8Epi gkv{MTFM_ACT_SILU, MTFM_BF16, 2, {0, Dkv, 2 * Dkv, 2 * Dkv, 2 * Dkv}, {bf(W.k), bf(W.v), nullptr, nullptr},
                      {Dkv, Dkv, 0, 0}, nullptr, 0, nullptr};
-    if ((e = launch_gemm_fp8(err, N, 2 * Dkv, d, in8(W.xn, W.xn_s, d), wt(w.w_kv), gkv, st)) != cudaSuccess) return e;
+    if ((e = launch_gemm_fp8(err, N, 2 * Dkv, d, xn, wt(w.w_kv), gkv, st)) != cudaSuccess) return e;
   }
   float* a = reinterpret_cast<float*>(ws + W.a);
   if ((e = launch_attn(r, m, L, target, bf(W.q), bf(W.k), bf(W.v), a, st)) != cudaSuccess) return e;

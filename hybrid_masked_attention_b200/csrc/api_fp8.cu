@@ -39,7 +39,7 @@ mtfm_status mtfm_add_rmsnorm_fp8(int32_t rows, int32_t dim, const void* d_x, int
   if (!scales_ok(d_scale, ld_scale, rows, ceil_div(dim, kGroup)) || !aligned(d_rstd, 4)) return MTFM_ERR_INVALID_ARG;
   return cuda_status(launch_add_rmsnorm_fp8(
       nullptr, rows, dim, MatIn{d_x, pitch(rows, ldx, dim), x_type}, MatIn{d_delta, pitch(rows, ld_delta, dim), delta_type},
-      nullptr, d_w, eps > 0.f ? eps : kRmsEps, MatOut{d_x_out, pitch(rows, ld_x_out, dim), x_type},
+      rows, nullptr, d_w, eps > 0.f ? eps : kRmsEps, MatOut{d_x_out, pitch(rows, ld_x_out, dim), x_type},
       Fp8Out{d_out, pitch(rows, ld_out, dim), d_scale, ld_scale}, d_rstd, static_cast<cudaStream_t>(stream)));
 }
 

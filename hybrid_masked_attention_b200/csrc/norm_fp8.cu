@@ -18,7 +18,8 @@
 namespace mtfm {
 namespace {
 
-struct None {};  // no delta
+struct None {};    // no delta
+struct Mapped {};  // no delta, and rows from `mapped` on gathered
 
 template <typename XT, typename DT>
 struct NormArgs {
@@ -28,6 +29,7 @@ struct NormArgs {
   int64_t ldx;
   const DT* delta;
   int64_t ld_delta;
+  int mapped;  // rows from this one on read row row_map[row - mapped] of x
   const int32_t* row_map;
   const float* w;
   float eps;
@@ -45,7 +47,8 @@ constexpr int kThreadsN = !MULTI ? 128 : C == 4 ? 256 : 512;
 template <typename XT, typename DT, int C, bool MULTI, bool VEC>
 __global__ void __launch_bounds__(kThreadsN<C, MULTI>)
 add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
-  constexpr bool kDelta = !std::is_same<DT, None>::value;
+  constexpr bool kMapped = std::is_same<DT, Mapped>::value;
+  constexpr bool kDelta = !kMapped && !std::is_same<DT, None>::value;
   using DRaw = typename std::conditional<kDelta, DT, XT>::type;
   constexpr int kWarps = kThreadsN<C, MULTI> / 32;
   __shared__ __align__(16) float s_part[2][kWarps];
@@ -61,7 +64,9 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
   Raw<DRaw> dr[C];
   auto load_row = [&](int64_t row) {
     if (row >= p.rows) return;
-    const XT* px = p.x + (p.row_map ? p.row_map[row] : row) * p.ldx;
+    int64_t src = row;
+    if constexpr (kMapped) src = row >= p.mapped ? (int64_t)p.row_map[row - p.mapped] : row;
+    const XT* px = p.x + src * p.ldx;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int g = i * W + sub;
@@ -171,10 +176,10 @@ cudaError_t shape(NormArgs<XT, DT>& a, cudaStream_t st) {
 }
 
 template <typename XT, typename DT>
-cudaError_t types(const int32_t* err, int rows, int dim, const MatIn& x, const MatIn& delta, const int32_t* row_map,
+cudaError_t types(const int32_t* err, int rows, int dim, const MatIn& x, const MatIn& delta, int mapped, const int32_t* row_map,
                   const float* w, float eps, const MatOut& x_out, const Fp8Out& out, float* rstd, cudaStream_t st) {
   NormArgs<XT, DT> a{err, rows, dim, 1, static_cast<const XT*>(x.p), x.ld, static_cast<const DT*>(delta.p), delta.ld,
-                     row_map, w, eps, static_cast<XT*>(x_out.p), x_out.ld, out, rstd};
+                     mapped, row_map, w, eps, static_cast<XT*>(x_out.p), x_out.ld, out, rstd};
   const bool vec = dim % 4 == 0 && rows_vec4(x.p, x.ld, sizeof(XT)) &&
                    (!delta.p || rows_vec4(delta.p, delta.ld, dtype_size(delta.type))) &&
                    (!x_out.p || rows_vec4(x_out.p, x_out.ld, sizeof(XT))) && rows_vec4(w, 4, 4) &&
@@ -183,7 +188,8 @@ cudaError_t types(const int32_t* err, int rows, int dim, const MatIn& x, const M
 }
 
 template <typename XT, typename... Args>
-cudaError_t with_delta(const MatIn& delta, Args&&... args) {
+cudaError_t with_delta(const MatIn& delta, const int32_t* row_map, Args&&... args) {
+  if (row_map) return types<XT, Mapped>(args...);
   if (!delta.p) return types<XT, None>(args...);
   if (delta.type == MTFM_BF16) return types<XT, __nv_bfloat16>(args...);
   return types<XT, float>(args...);
@@ -192,12 +198,12 @@ cudaError_t with_delta(const MatIn& delta, Args&&... args) {
 }  // namespace
 
 cudaError_t launch_add_rmsnorm_fp8(const int32_t* err, int rows, int dim, const MatIn& x, const MatIn& delta,
-                                   const int32_t* row_map, const float* w, float eps, const MatOut& x_out,
+                                   int mapped, const int32_t* row_map, const float* w, float eps, const MatOut& x_out,
                                    const Fp8Out& out, float* rstd, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   if (x.type == MTFM_BF16)
-    return with_delta<__nv_bfloat16>(delta, err, rows, dim, x, delta, row_map, w, eps, x_out, out, rstd, st);
-  return with_delta<float>(delta, err, rows, dim, x, delta, row_map, w, eps, x_out, out, rstd, st);
+    return with_delta<__nv_bfloat16>(delta, row_map, err, rows, dim, x, delta, mapped, row_map, w, eps, x_out, out, rstd, st);
+  return with_delta<float>(delta, row_map, err, rows, dim, x, delta, mapped, row_map, w, eps, x_out, out, rstd, st);
 }
 
 }  // namespace mtfm
