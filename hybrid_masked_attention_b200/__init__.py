@@ -709,9 +709,7 @@ def gate_fwd_fp8(cfg, meta, target: bool, a, u, gamma, beta, out, scale, stats, 
             raise MtfmError(st, "mtfm_gate_fwd_fp8")
     rows, D = cfg.total_t if target else cfg.total_tokens, cfg.D
     dev = _device_of(a, "a")
-    for t, name in ((meta, "meta"), (u, "u"), (gamma, "gamma"), (beta, "beta"), (stats, "stats")):
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on device {dev}, got {t.device}")
+    _same_device(dev, meta=meta, u=u, gamma=gamma, beta=beta, stats=stats)
     pq, ldq = _mat(out, "out", dev, rows, D, _F8)
     ps, lds = _mat(scale, "scale", dev, rows, _groups(D), _F32)
     _run_on(dev, stream, "mtfm_gate_fwd_fp8", _lib.mtfm_gate_fwd_fp8, ctypes.byref(c), _ptr(meta, torch.uint8, None, "meta"),
@@ -769,6 +767,8 @@ def fp8_gemm(a, a_scale, b, b_scale, out, status, act: Optional[str] = None, res
 
 def fp8_check(status, stream=None):
     """Synchronises the stream; raises MtfmError if a product on this status word failed."""
+    if not status.is_cuda:
+        raise ValueError("status must be a CUDA tensor")
     dev = status.get_device()
     _run_on(dev, stream, "mtfm_fp8_check", _lib.mtfm_fp8_check, _vec(status, "status", dev, 1, torch.int32))
 
@@ -804,8 +804,15 @@ def _fp8_weight(pair, name, dev, rows, cols) -> CFp8Weight:
     return CFp8Weight(pq, ldq, ps, lds)
 
 
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on device {dev}, got {t.device}")
+
+
 def _fp8_layer_struct(cfg: Config, d_model: int, w: Fp8LayerWeights, dev) -> CFp8LayerWeights:
     D, Dkv = cfg.D, cfg.Dkv
+    _same_device(dev, rms_w=w.rms_w, gamma=w.gamma, beta=w.beta)
     if w.kind not in ("F", "T"):
         raise ValueError("layer kind must be 'F' or 'T'")
     target = w.kind == "T"
@@ -831,6 +838,7 @@ def fp8_layer_fwd(cfg: Config, meta, d_model: int, w: Fp8LayerWeights, x, ws, st
     """layer_fwd with 8-bit projections: X (fp32 [total_tokens, d_model]) updated in place."""
     c = cfg.c()
     dev = _device_of(x, "x")
+    _same_device(dev, meta=meta, ws=ws)
     lw = _fp8_layer_struct(cfg, d_model, w, dev)
     _run_on(dev, stream, "mtfm_fp8_layer_fwd", _lib.mtfm_fp8_layer_fwd, ctypes.byref(c), _ptr(meta, torch.uint8, name="meta"),
             int(d_model), int(w.kind == "T"), ctypes.byref(lw), _ptr(x, _F32, (cfg.total_tokens, d_model), "x"),
@@ -841,6 +849,7 @@ def fp8_stack_fwd(cfg: Config, meta, d_model: int, layers, x, ws, stream=None):
     """Run ``layers`` (a list of Fp8LayerWeights) on X in place."""
     c = cfg.c()
     dev = _device_of(x, "x")
+    _same_device(dev, meta=meta, ws=ws)
     arr = (CFp8LayerWeights * max(1, len(layers)))(*[_fp8_layer_struct(cfg, d_model, w, dev) for w in layers])
     kinds = "".join(w.kind for w in layers).encode()
     _run_on(dev, stream, "mtfm_fp8_stack_fwd", _lib.mtfm_fp8_stack_fwd, ctypes.byref(c), _ptr(meta, torch.uint8, name="meta"),

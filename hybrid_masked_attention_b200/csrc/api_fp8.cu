@@ -87,7 +87,7 @@ mtfm_status mtfm_fp8_gemm(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, i
                           int32_t out_type, int64_t ld_out, int32_t* d_status, void* stream) {
   if (m < 0 || n < 0 || k <= 0) return MTFM_ERR_INVALID_ARG;
   if (act != MTFM_ACT_NONE && act != MTFM_ACT_SILU) return MTFM_ERR_INVALID_ARG;
-  constexpr int32_t kMost = 2147483647 - 1024;  // tile coordinates stay int32
+  constexpr int32_t kMost = 2147483647 - 8192;  // tile coordinates stay int32
   if (m > kMost || n > kMost || k > kMost) return MTFM_ERR_UNSUPPORTED;
   if (m == 0 || n == 0) return MTFM_OK;
   if (!d_a || !d_b || !aligned(d_a, 16) || !aligned(d_b, 16)) return MTFM_ERR_INVALID_ARG;
@@ -99,6 +99,7 @@ mtfm_status mtfm_fp8_gemm(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, i
     return MTFM_ERR_INVALID_ARG;
   if (!mat_ok(d_out, out_type, ld_out, m, n) || (d_res && !mat_ok(d_res, out_type, ld_res, m, n)))
     return MTFM_ERR_INVALID_ARG;
+  if (d_res == d_out && m > 1 && ld_res != ld_out) return MTFM_ERR_INVALID_ARG;  // in place: the same rows
   if (!d_status || !aligned(d_status, 4)) return MTFM_ERR_INVALID_ARG;
   const Fp8Epi epi{act, out_type, 1, {0, n, n, n, n}, {d_out, nullptr, nullptr, nullptr},
                    {pitch(m, ld_out, n), 0, 0, 0}, d_res, pitch(m, ld_res, n), nullptr};

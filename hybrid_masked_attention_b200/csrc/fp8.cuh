@@ -209,8 +209,8 @@ inline int dtype_size(int type) { return type == MTFM_BF16 ? 2 : 4; }
 cudaError_t launch_add_rmsnorm_fp8(const int32_t* err, int rows, int dim, const MatIn& x, const MatIn& delta,
                                    int mapped, const int32_t* row_map, const float* w, float eps, const MatOut& x_out,
                                    const Fp8Out& out, float* rstd, cudaStream_t st);
-// Blocks of the backward's row pass: each writes one partial row of dw.
-constexpr int kNormBwdBlocks = 592;
+// Blocks of the backward's row pass at most (2 an SM of 148): each writes one partial row of dw.
+constexpr int kNormBwdBlocks = 296;
 cudaError_t launch_rmsnorm_bwd(int rows, int dim, const MatIn& x, const float* w, const float* rstd, const MatIn& dy,
                                const MatIn& dres, const MatOut& dx, float* dw, float* partials, cudaStream_t st);
 cudaError_t launch_gate_fwd_fp8(const MetaView& m, bool target, int rows, int D, float eps, const float* a,

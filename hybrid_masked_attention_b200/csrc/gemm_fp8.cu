@@ -307,6 +307,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
   volatile int* abort_flag = &bars.abort;
+  pdl_trigger();  // where this grid leaves SMs free, the next kernel sets itself up there meanwhile
   const bool skip = ld_cluster(map_rank(smem_addr(&bars.skip), 0)) != 0;
   const int first = skip ? n_tiles : (int)(blockIdx.x >> 1);
 
@@ -330,10 +331,11 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           const uint32_t full = full0 + (uint32_t)s * 8;
           // boxes that reach past a matrix are filled with zeros and count in full
           if (rank == 0) mbar_expect_tx((b_full + s * 8), 2 * kStage);
-          tma_load_pair(sbase + s * kStage, &tm_a, full, kb * kGroup, m0);
+          if (load_ok(p.err, kb * kGroup, p.K, 1, m0)) tma_load_pair(sbase + s * kStage, &tm_a, full, kb * kGroup, m0);
 #pragma unroll
           for (int part = 0; part < kParts; ++part)  // this CTA's 64 of the part's 128 rows of B
-            tma_load_pair(sbase + s * kStage + kABytes + part * (64 * kGroup), &tm_b, full, kb * kGroup, n0 + part * 128);
+            if (load_ok(p.err, kb * kGroup, p.K, 1, n0 + part * 128))
+              tma_load_pair(sbase + s * kStage + kABytes + part * (64 * kGroup), &tm_b, full, kb * kGroup, n0 + part * 128);
           ++issued;
           if (++s == kStages) {
             s = 0;
@@ -479,7 +481,9 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         bulk_wait_read<0>();  // the last tile's stores have read the staging
         mbar_expect_tx(b_res, kResBytes);
 #pragma unroll
-        for (int b = 0; b < kResBoxes; ++b) tma_load_2d(sstage + b * kBoxBytes, &tm_o1, b_res, col0 + b * kOutCols, m0);
+        for (int b = 0; b < kResBoxes; ++b)
+          if (load_ok(p.err, col0 + b * kOutCols, nN * BN, (int)sizeof(OT), m0))
+            tma_load_2d(sstage + b * kBoxBytes, &tm_o1, b_res, col0 + b * kOutCols, m0);
         ++res_issued;
       }
       float2 acc[kCols / 2];
@@ -566,7 +570,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         if (issuer && ok && m0 < p.M) {
 #pragma unroll
           for (int b = 0; b < kResBoxes; ++b)
-            if (col0 + b * kOutCols < p.N) tma_store_2d(&tm_o0, sstage + b * kBoxBytes, col0 + b * kOutCols, m0);
+            if (col0 + b * kOutCols < p.N && store_ok(p.err, col0 + b * kOutCols, p.N, (int)sizeof(OT), m0, p.M))
+              tma_store_2d(&tm_o0, sstage + b * kBoxBytes, col0 + b * kOutCols, m0);
           bulk_commit();
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -613,7 +618,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                   begin = p.epi.seg_begin[q];
                   om = q == 1 ? &tm_o1 : q == 2 ? &tm_o2 : &tm_o3;
                 }
-              tma_store_2d(om, sstage, col - begin, m0);
+              if (store_ok(p.err, col - begin, p.N, (int)sizeof(OT), m0, p.M)) tma_store_2d(om, sstage, col - begin, m0);
               bulk_commit();
             }
           } else {
@@ -672,7 +677,6 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       }
     }
   }
-  pdl_trigger();
   __syncthreads();
   cluster_sync();  // the other CTA's MMAs, copies and arrivals reach into this one
   if (warp == 1) {

@@ -15,6 +15,25 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Test of a TMA coordinate in the bounds-checked build (MTFM_DEBUG_BOUNDS, mtfm_internal.cuh): a
+// failed one sets the error word, and the caller skips the copy.  `true` in other builds.
+__device__ __forceinline__ bool tma_inbounds(int32_t* err, bool ok) {
+#ifdef MTFM_DEBUG_BOUNDS
+  if (!ok) atomicOr(err, kErrBounds);
+  return ok;
+#else
+  return true;
+#endif
+}
+// A load's box may reach past its matrix, in x and y; its start is aligned, and not negative.
+__device__ __forceinline__ bool load_ok(int32_t* err, int x, int cols, int size, int y) {
+  return tma_inbounds(err, x >= 0 && (int64_t)x * size % 16 == 0 && x < cols && y >= 0);
+}
+// A store starts inside its matrix.
+__device__ __forceinline__ bool store_ok(int32_t* err, int x, int cols, int size, int y, int rows) {
+  return tma_inbounds(err, x >= 0 && (int64_t)x * size % 16 == 0 && x < cols && y >= 0 && y < rows);
+}
+
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;

@@ -113,6 +113,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
   pdl_wait();
   const bool skip = *p.err != 0;  // an earlier kernel on this error word failed
   __syncthreads();
+  pdl_trigger();  // where this grid leaves SMs free, the next kernel sets itself up there meanwhile
   if (S > 1) cluster_arrive();  // this CTA has started: its peers may store into it once they have waited
   tc_fence_after();
   const uint32_t tmem = s_tmem;
@@ -130,7 +131,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
         if (!mbar_wait(b_empty(s), ph ^ 1, abort_flag)) break;
         // boxes that reach past a matrix are filled with zeros and count in full
         mbar_expect_tx(b_full(s), kStage);
-        tma_load_2d(sbase + s * kStage, &tm_w, b_full(s), kb * kGroup, n0);
+        if (load_ok(p.err, kb * kGroup, p.K, 1, n0)) tma_load_2d(sbase + s * kStage, &tm_w, b_full(s), kb * kGroup, n0);
         tma_load_2d(sbase + s * kStage + kWBytes, &tm_x, b_full(s), kb * kGroup, 0);
         if (++s == kStages) {
           s = 0;
@@ -248,7 +249,6 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
     cluster_arrive();
     cluster_wait();  // the partial sums have arrived; no CTA leaves before its peers' stores
   }
-  pdl_trigger();
   if (warp >= 2 && !skip) {
     // ------------------------------------------------------------- epilogue
     const int r_in = (warp & 3) * 32 + lane;

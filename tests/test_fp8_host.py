@@ -73,7 +73,7 @@ GEMM = dict(m=200, n=300, k=400, a=P, lda=400, sa=P, ldsa=4, b=P, ldb=400, sb=P,
     (dict(a=None), 1), (dict(a=P + 8), 1), (dict(lda=399), 1), (dict(lda=408), 1), (dict(lda=384), 1), (dict(b=None), 1),
     (dict(b=P + 4), 1), (dict(ldb=401), 1), (dict(sa=None), 1), (dict(ldsa=3), 1), (dict(sb=None), 1), (dict(ldsb=3), 1),
     (dict(sb=P + 2), 1), (dict(out=None), 1), (dict(ot=2), 1), (dict(ldo=299), 1), (dict(out=P + 2), 1), (dict(res=P, ldr=299), 1),
-    (dict(res=P + 1, ldr=300), 1), (dict(st=None), 1), (dict(st=P + 2), 1), (dict(m=0, a=None, out=None), 0),
+    (dict(res=P + 1, ldr=300), 1), (dict(res=P, ldr=304), 1), (dict(st=None), 1), (dict(st=P + 2), 1), (dict(m=0, a=None, out=None), 0),
     (dict(n=0, b=None, out=None), 0),
 ])
 def test_gemm_refusals(m, kw, status):
@@ -129,6 +129,7 @@ def test_wrappers_refuse_host_tensors(m):
     q, s = torch.zeros(4, 64).to(torch.float8_e4m3fn), torch.zeros(4, 1)
     for call in (lambda: m.fp8_quant(x, q, s), lambda: m.add_rmsnorm_fp8(x, None, torch.ones(64), None, q, s),
                  lambda: m.fp8_gemm(q, s, q, s, x, torch.zeros(1, dtype=torch.int32)),
+                 lambda: m.fp8_check(torch.zeros(1, dtype=torch.int32)),
                  lambda: m.rmsnorm_bwd(x, torch.ones(64), torch.ones(4), x, None, x, torch.ones(64), torch.zeros(8, dtype=torch.uint8))):
         with pytest.raises(ValueError, match="CUDA"):
             call()

@@ -386,9 +386,56 @@ def test_gemm_status_word_stops_later_calls(cuda_ok):
     with pytest.raises(M.MtfmError) as e:
         M.fp8_check(status)
     assert e.value.status == 6
-    a, sa, b, sb = operands(0, 64, 128) if False else (a, sa, b, sb)
     status.zero_()
     M.fp8_gemm(a[:0], sa[:0], b, sb, out[:0], status)
+    M.fp8_check(status)
+
+
+def test_offsets_past_31_bits(cuda_ok):
+    """More than 2^31 elements: the last rows of the quantiser, the norm and the product."""
+    import hybrid_masked_attention_b200 as M
+    rows, cols = 140_000, 16_384
+    x = torch.empty(rows, cols, dtype=BF16, device="cuda")
+    x[-3:] = rnd(61, 3, cols, dtype=BF16)
+    x[:-3] = 1.0
+    q, s = torch.empty(rows, cols, dtype=F8, device="cuda"), torch.empty(rows, cols // 128, device="cuda")
+    M.fp8_quant(x, q, s)
+    R.check_quant(q[-3:], s[-3:], x[-3:].double(), 0.0)
+    w = 1 + 0.1 * rnd(62, cols)
+    M.add_rmsnorm_fp8(x, None, w, None, q, s)
+    _, _, v = R.add_rmsnorm(x[-3:], None, w, 1e-6)
+    R.check_quant(q[-3:], s[-3:], v, v.abs() * 64 * U)
+    a, sa, b, sb = operands(rows, cols, 128)
+    out, status = x, torch.zeros(1, dtype=torch.int32, device="cuda")
+    M.fp8_gemm(a, sa, b, sb, out, status)
+    M.fp8_check(status)
+    check_gemm(out[-130:], a[-130:], sa[-130:], b, sb, None, None)
+
+
+def test_two_streams_at_once(cuda_ok):
+    """Products and norms in flight on two streams, sharing a status word: each as if alone."""
+    import hybrid_masked_attention_b200 as M
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    jobs = [(operands(m, n, k, seed), torch.empty(m, n, device="cuda")) for m, n, k, seed in
+            ((700, 1280, 512, 71), (20, 4096, 2048, 75), (900, 640, 1024, 79), (9, 1280, 512, 83))]
+    want = []
+    for ops, out in jobs:
+        M.fp8_gemm(*ops, out, status)
+        want.append(out.clone())
+        out.zero_()
+    x, w = rnd(87, 3000, 512), torch.ones(512, device="cuda")
+    q, s = out8(3000, 512)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(10):
+        for i, (ops, out) in enumerate(jobs):
+            M.fp8_gemm(*ops, out, status, stream=streams[(i + rep) % 2])
+        M.add_rmsnorm_fp8(x, None, w, None, q, s, stream=streams[rep % 2])
+        torch.cuda.synchronize()
+        for (_, out), t in zip(jobs, want):
+            assert torch.equal(out, t)
+            out.zero_()
+        torch.cuda.synchronize()
     M.fp8_check(status)
 
 

@@ -211,3 +211,21 @@ def test_training_step_of_a_projection(rows, cuda_ok):
     torch.cuda.synchronize()
     for t, k in zip((y, dx, dw), keep):
         assert torch.equal(t, k)
+
+
+def test_under_bounds_checked_build(cuda_ok):
+    """The product's and the layers' small cases under the bounds-checked build, which tests every
+    TMA coordinate: a failed test would set the error words that these cases check."""
+    import os
+    import subprocess
+    import sys
+    if os.environ.get("MTFM_LIBRARY"):
+        pytest.skip("already running under another build")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, os.path.join(root, "hybrid_masked_attention_b200"))
+    import build
+    env = dict(os.environ, MTFM_LIBRARY=build.build(debug_bounds=True))
+    r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_gpu_fp8.py", "tests/test_gpu_fp8_stack.py", "-q", "-x", "-m",
+                        "gpu", "-k", "test_gemm or tiny or edge or training", "-p", "no:cacheprovider"],
+                       cwd=root, env=env, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and " passed" in r.stdout, (r.stdout + r.stderr)[-3000:]
