@@ -30,6 +30,15 @@ struct BwdArgs {
   float* partials;
 };
 
+__device__ __forceinline__ void unpack2(const Raw<float>& r, float2 (&v)[2]) {
+  v[0] = make_float2(r.v.x, r.v.y);
+  v[1] = make_float2(r.v.z, r.v.w);
+}
+__device__ __forceinline__ void unpack2(const Raw<__nv_bfloat16>& r, float2 (&v)[2]) {
+  v[0] = make_float2(__uint_as_float(r.v.x << 16), __uint_as_float(r.v.x & 0xffff0000u));
+  v[1] = make_float2(__uint_as_float(r.v.y << 16), __uint_as_float(r.v.y & 0xffff0000u));
+}
+
 // C groups a warp: 4 with the next row's loads in flight (blocks of 8 warps, rows of up to
 // 4096 columns), 8 without (16 warps, 16384 columns; 128 registers do not hold a second row).
 template <int C>
@@ -46,15 +55,14 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
   __shared__ __align__(16) float s_part[2][kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int W = p.W, sub = warp % W, slot = warp / W, R = kWarps / W;
-  const int G = (p.dim + kGroup - 1) / kGroup;
+  // the warp's C groups are neighbours: their addresses differ by constants
+  const int col0 = sub * C * kGroup, n0 = p.dim - col0;  // first column, and columns from there on
   pdl_wait();
   pdl_trigger();
   const float inv_dim = 1.f / (float)p.dim;
-  float dw[C][4];
+  float2 dw[C][2];
 #pragma unroll
-  for (int i = 0; i < C; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dw[i][j] = 0.f;
+  for (int i = 0; i < C; ++i) dw[i][0] = dw[i][1] = make_float2(0.f, 0.f);
   Raw<XT> xr[C];
   Raw<YT> yr[C];
   Raw<RRaw> rr[C];
@@ -62,14 +70,21 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
   auto load_row = [&](int64_t row) {
     if (row >= p.rows) return;
     r_next = p.rstd[row];
+    const XT* px = p.x + row * p.ldx + col0;
+    const YT* py = p.dy + row * p.ld_dy + col0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int g = i * W + sub;
-      if (g < G) {
-        xr[i] = load_raw<VEC>(p.x + row * p.ldx + g * kGroup, lane, p.dim - g * kGroup);
-        yr[i] = load_raw<VEC>(p.dy + row * p.ld_dy + g * kGroup, lane, p.dim - g * kGroup);
-        if constexpr (kRes && kAhead) rr[i] = load_raw<VEC>(p.dres + row * p.ld_dres + g * kGroup, lane, p.dim - g * kGroup);
+      const int n = n0 - i * kGroup;
+      if (n > 0) {
+        xr[i] = load_raw<VEC>(px + i * kGroup, lane, n);
+        yr[i] = load_raw<VEC>(py + i * kGroup, lane, n);
       }
+    }
+    if constexpr (kRes && kAhead) {
+      const RT* pr = p.dres + row * p.ld_dres + col0;
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (n0 - i * kGroup > 0) rr[i] = load_raw<VEC>(pr + i * kGroup, lane, n0 - i * kGroup);
     }
   };
   const int64_t step = (int64_t)gridDim.x * R;
@@ -81,30 +96,32 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
     const bool live = row < p.rows;
     if (!kAhead) load_row(row);
     const float r = r_next;
-    float xv[C][4], gv[C][4];
+    float2 xv[C][2], gv[C][2];
+    const float2 r2 = make_float2(r, r);
+    float2 s2 = make_float2(0.f, 0.f);
     Raw<RRaw> res[C];
     float s = 0.f;
     if (live) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const int g = i * W + sub;
-        if (g < G) {
-          unpack(xr[i], xv[i]);
-          unpack(yr[i], gv[i]);
+        const int n = n0 - i * kGroup;
+        if (n > 0) {
+          unpack2(xr[i], xv[i]);
+          unpack2(yr[i], gv[i]);
           res[i] = rr[i];
-          float ww[4];
-          load4<VEC>(p.w + g * kGroup, lane, p.dim - g * kGroup, ww);
+          float2 ww[2];
+          unpack2(load_raw<VEC>(p.w + col0 + i * kGroup, lane, n), ww);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            dw[i][j] = fmaf(gv[i][j], xv[i][j] * r, dw[i][j]);
-            gv[i][j] *= ww[j];
-            s = fmaf(gv[i][j], xv[i][j], s);
+          for (int j = 0; j < 2; ++j) {  // two columns an instruction
+            dw[i][j] = __ffma2_rn(gv[i][j], __fmul2_rn(xv[i][j], r2), dw[i][j]);
+            gv[i][j] = __fmul2_rn(gv[i][j], ww[j]);
+            s2 = __ffma2_rn(gv[i][j], xv[i][j], s2);
           }
         }
       }
     }
     if (kAhead) load_row(row + step);
-    s = warp_sum32(s);
+    s = warp_sum32(s2.x + s2.y);
     if (W > 1) {
       if (lane == 0) s_part[flip][warp] = s;
       __syncthreads();
@@ -112,22 +129,24 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
     }
     if (live) {
       const float c = s * inv_dim * r * r;
+      const float2 c2 = make_float2(-c, -c);
+      XT* pdx = p.dx + row * p.ld_dx + col0;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const int g = i * W + sub;
-        if (g < G) {
-          const int n = p.dim - g * kGroup;
-          float o[4];
+        const int n = n0 - i * kGroup;
+        if (n > 0) {
+          float2 o[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = r * fmaf(-xv[i][j], c, gv[i][j]);
+          for (int j = 0; j < 2; ++j) o[j] = __fmul2_rn(r2, __ffma2_rn(xv[i][j], c2, gv[i][j]));
           if constexpr (kRes) {
-            float t[4];
-            if constexpr (kAhead) unpack(res[i], t);
-            else load4<VEC>(p.dres + row * p.ld_dres + g * kGroup, lane, n, t);
+            float2 t[2];
+            if constexpr (kAhead) unpack2(res[i], t);
+            else unpack2(load_raw<VEC>(p.dres + row * p.ld_dres + col0 + i * kGroup, lane, n), t);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] += t[j];
+            for (int j = 0; j < 2; ++j) o[j] = __fadd2_rn(o[j], t[j]);
           }
-          put4<VEC>(p.dx + row * p.ld_dx + g * kGroup, lane, n, o);
+          const float ov[4] = {o[0].x, o[0].y, o[1].x, o[1].y};
+          put4<VEC>(pdx + i * kGroup, lane, n, ov);
         }
       }
     }
@@ -137,12 +156,10 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
     if (slot > 0)
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const int g = i * W + sub;
-        if (g < G)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int c = g * kGroup + lane_col<VEC>(lane, j);
-            if (c < p.dim) s_dw[(size_t)(slot - 1) * p.dim + c] = dw[i][j];
+        for (int j = 0; j < 4; ++j) {
+            const int c = col0 + i * kGroup + lane_col<VEC>(lane, j);
+            if (c < p.dim) s_dw[(size_t)(slot - 1) * p.dim + c] = j & 1 ? dw[i][j >> 1].y : dw[i][j >> 1].x;
           }
       }
     __syncthreads();
@@ -150,13 +167,11 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
   if (slot == 0)
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int g = i * W + sub;
-      if (g < G)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = g * kGroup + lane_col<VEC>(lane, j);
+      for (int j = 0; j < 4; ++j) {
+          const int c = col0 + i * kGroup + lane_col<VEC>(lane, j);
           if (c < p.dim) {
-            float t = dw[i][j];
+            float t = j & 1 ? dw[i][j >> 1].y : dw[i][j >> 1].x;
             for (int k = 0; k < R - 1; ++k) t += s_dw[(size_t)k * p.dim + c];
             p.partials[(size_t)blockIdx.x * p.dim + c] = t;
           }

@@ -56,7 +56,8 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
   const int W = MULTI ? p.W : 1;
   const int sub = MULTI ? warp % W : 0, slot = MULTI ? warp / W : warp;
   const int R = kWarps / W;  // rows of a block at a time
-  const int G = (p.dim + kGroup - 1) / kGroup;
+  // the warp's C groups are neighbours: their addresses differ by constants
+  const int col0 = sub * C * kGroup, n0 = p.dim - col0;  // first column, and columns from there on
   pdl_wait();
   pdl_trigger();
   if (p.err && *p.err) return;
@@ -66,19 +67,15 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
     if (row >= p.rows) return;
     int64_t src = row;
     if constexpr (kMapped) src = row >= p.mapped ? (int64_t)p.row_map[row - p.mapped] : row;
-    const XT* px = p.x + src * p.ldx;
+    const XT* px = p.x + src * p.ldx + col0;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int g = i * W + sub;
-      if (g < G) xr[i] = load_raw<VEC>(px + g * kGroup, lane, p.dim - g * kGroup);
-    }
+    for (int i = 0; i < C; ++i)
+      if (n0 - i * kGroup > 0) xr[i] = load_raw<VEC>(px + i * kGroup, lane, n0 - i * kGroup);
     if constexpr (kDelta) {
-      const DT* pd = p.delta + row * p.ld_delta;
+      const DT* pd = p.delta + row * p.ld_delta + col0;
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int g = i * W + sub;
-        if (g < G) dr[i] = load_raw<VEC>(pd + g * kGroup, lane, p.dim - g * kGroup);
-      }
+      for (int i = 0; i < C; ++i)
+        if (n0 - i * kGroup > 0) dr[i] = load_raw<VEC>(pd + i * kGroup, lane, n0 - i * kGroup);
     }
   };
   const int64_t step = (int64_t)gridDim.x * R;
@@ -91,7 +88,7 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      if (i * W + sub < G) {
+      if (n0 - i * kGroup > 0) {
         unpack(xr[i], h[i]);
         if constexpr (kDelta) {
           float d[4];
@@ -113,23 +110,24 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
     if (row >= p.rows) continue;
     const float r = 1.f / sqrtf(s / (float)p.dim + p.eps);
     if (p.rstd && sub == 0 && lane == 0) p.rstd[row] = r;
-    uint8_t* qr = p.out.q + row * p.out.ld;
+    uint8_t* qr = p.out.q + row * p.out.ld + col0;
+    XT* xo = p.x_out + row * p.ld_xout + col0;
+    const float* pw = p.w + col0;
     float mine = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int g = i * W + sub;
-      if (g < G) {
-        const int n = p.dim - g * kGroup;
-        if (kDelta && p.x_out) put4<VEC>(p.x_out + row * p.ld_xout + g * kGroup, lane, n, h[i]);
+      const int n = n0 - i * kGroup;
+      if (n > 0) {
+        if (kDelta && p.x_out) put4<VEC>(xo + i * kGroup, lane, n, h[i]);
         float ww[4], v[4];
-        load4<VEC>(p.w + g * kGroup, lane, n, ww);
+        load4<VEC>(pw + i * kGroup, lane, n, ww);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = h[i][j] * r * ww[j];
-        const float m = quant_group<VEC>(v, lane, n, qr + g * kGroup);
+        const float m = quant_group<VEC>(v, lane, n, qr + i * kGroup);
         if (lane == i) mine = m;
       }
     }
-    if (lane < C && lane * W + sub < G) p.out.scale[row * p.out.ld_scale + lane * W + sub] = mine / kE4m3Max;
+    if (lane < C && n0 > lane * kGroup) p.out.scale[row * p.out.ld_scale + sub * C + lane] = mine / kE4m3Max;
   }
 }
 
