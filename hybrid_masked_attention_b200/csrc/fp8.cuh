@@ -45,7 +45,7 @@ __device__ __forceinline__ float warp_sum32(float x) {
 // Index of the warp in its block, known to the compiler as equal in all of its lanes: row
 // pointers then live in uniform registers.  The quantiser's time was mostly address arithmetic
 // (12345 x 1000 bf16: 12.6 us, with it 9.6); the norm, whose next row is loaded under a
-// condition, lost its overlap by it (57023 x 768: 84 us without, 110 with).
+// condition, lost its overlap by it and a quarter of its speed.
 __device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
 
 // 1 / x to one unit in the last place, subnormal results included.
@@ -55,7 +55,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// Sum of the partial sums of a row's W warps (a power of two), in their order.
+// Sum of the partial sums of a row's W warps (a power of two, at least 2), in their order.
 __device__ __forceinline__ float row_sum(const float* part, int W) {
   if (W < 4) return part[0] + part[1];
   float s = 0.f;
@@ -70,12 +70,17 @@ __device__ __forceinline__ float row_sum(const float* part, int W) {
 // VEC (rows of a multiple of 4 columns that start on 4-element boundaries): columns 4 lane ..
 // 4 lane + 3 as one vector.  Otherwise columns lane, lane + 32, lane + 64, lane + 96, which
 // keeps element-wise accesses coalesced for rows at any offset.
-template <typename T>
-struct Raw;  // four elements as they are in memory
+// Raw: the four elements as loaded.  Nothing is computed from them before unpack(), so that a row
+// fetched ahead stays in flight (with single bf16 loads packed into words at once, the backward of
+// 30000 x 1001 took 107 us; without, 68).
+template <typename T, bool VEC>
+struct Raw;
+template <bool VEC>
+struct Raw<float, VEC> { float4 v; };
 template <>
-struct Raw<float> { float4 v; };
+struct Raw<__nv_bfloat16, true> { uint2 v; };
 template <>
-struct Raw<__nv_bfloat16> { uint2 v; };
+struct Raw<__nv_bfloat16, false> { uint16_t v[4]; };
 
 template <bool VEC>
 __device__ __forceinline__ bool lane_has(int lane, int j, int n) { return (VEC ? 4 * lane : lane + 32 * j) < n; }
@@ -83,8 +88,8 @@ template <bool VEC>
 __device__ __forceinline__ int lane_col(int lane, int j) { return VEC ? 4 * lane + j : lane + 32 * j; }
 
 template <bool VEC>
-__device__ __forceinline__ Raw<float> load_raw(const float* p, int lane, int n) {
-  Raw<float> r{make_float4(0.f, 0.f, 0.f, 0.f)};
+__device__ __forceinline__ Raw<float, VEC> load_raw(const float* p, int lane, int n) {
+  Raw<float, VEC> r{make_float4(0.f, 0.f, 0.f, 0.f)};
   if (VEC) {
     if (4 * lane < n) r.v = *reinterpret_cast<const float4*>(p + 4 * lane);
   } else {
@@ -96,31 +101,50 @@ __device__ __forceinline__ Raw<float> load_raw(const float* p, int lane, int n) 
   return r;
 }
 template <bool VEC>
-__device__ __forceinline__ Raw<__nv_bfloat16> load_raw(const __nv_bfloat16* p, int lane, int n) {
-  Raw<__nv_bfloat16> r{make_uint2(0, 0)};
-  if (VEC) {
+__device__ __forceinline__ Raw<__nv_bfloat16, VEC> load_raw(const __nv_bfloat16* p, int lane, int n) {
+  Raw<__nv_bfloat16, VEC> r;
+  if constexpr (VEC) {
+    r.v = make_uint2(0, 0);
     if (4 * lane < n) r.v = *reinterpret_cast<const uint2*>(p + 4 * lane);
   } else {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-    uint32_t t[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) t[j] = lane + 32 * j < n ? h[lane + 32 * j] : 0;
-    r.v = make_uint2(t[0] | (t[1] << 16), t[2] | (t[3] << 16));
+    for (int j = 0; j < 4; ++j) r.v[j] = lane + 32 * j < n ? h[lane + 32 * j] : 0;
   }
   return r;
 }
-__device__ __forceinline__ void unpack(const Raw<float>& r, float (&v)[4]) {
+template <bool VEC>
+__device__ __forceinline__ void unpack(const Raw<float, VEC>& r, float (&v)[4]) {
   v[0] = r.v.x; v[1] = r.v.y; v[2] = r.v.z; v[3] = r.v.w;
 }
-__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, float (&v)[4]) {
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, true>& r, float (&v)[4]) {
   v[0] = __uint_as_float(r.v.x << 16);
   v[1] = __uint_as_float(r.v.x & 0xffff0000u);
   v[2] = __uint_as_float(r.v.y << 16);
   v[3] = __uint_as_float(r.v.y & 0xffff0000u);
 }
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, false>& r, float (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = __uint_as_float((uint32_t)r.v[j] << 16);
+}
 template <bool VEC, typename T>
 __device__ __forceinline__ void load4(const T* p, int lane, int n, float (&v)[4]) {
   unpack(load_raw<VEC>(p, lane, n), v);
+}
+// The same of an array that nothing writes meanwhile (a norm's weight): such loads may move up
+// past the stores of other columns, which they otherwise wait behind one group after the other.
+template <bool VEC>
+__device__ __forceinline__ Raw<float, VEC> load_const(const float* p, int lane, int n) {
+  Raw<float, VEC> r{make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (VEC) {
+    if (4 * lane < n) r.v = __ldg(reinterpret_cast<const float4*>(p + 4 * lane));
+  } else {
+    if (lane < n) r.v.x = __ldg(p + lane);
+    if (lane + 32 < n) r.v.y = __ldg(p + lane + 32);
+    if (lane + 64 < n) r.v.z = __ldg(p + lane + 64);
+    if (lane + 96 < n) r.v.w = __ldg(p + lane + 96);
+  }
+  return r;
 }
 template <bool VEC>
 __device__ __forceinline__ void put4(float* p, int lane, int n, const float (&v)[4]) {
@@ -204,7 +228,7 @@ inline int dtype_size(int type) { return type == MTFM_BF16 ? 2 : 4; }
 
 // err (may be NULL): a device error word; the kernel does nothing while it is not zero.
 // With a row_map, rows from `mapped` on read row row_map[row - mapped] of x (a kernel of its own:
-// the test in the other one's loads took 57023 x 768 from 84 to 115 us); delta and x_out must
+// the test in the other one's loads cost it a third of its speed); delta and x_out must
 // then be NULL.
 cudaError_t launch_add_rmsnorm_fp8(const int32_t* err, int rows, int dim, const MatIn& x, const MatIn& delta,
                                    int mapped, const int32_t* row_map, const float* w, float eps, const MatOut& x_out,

@@ -25,8 +25,8 @@ gate_fwd_fp8_kernel(const MetaHeader* hdr, const uint8_t* __restrict__ row_type,
   pdl_wait();
   pdl_trigger();
   if (hdr->error) return;
-  Raw<float> ar[C];
-  Raw<__nv_bfloat16> ur[C];
+  Raw<float, true> ar[C];
+  Raw<__nv_bfloat16, true> ur[C];
   int type_next = kRowT;
   auto load_row = [&](int64_t row) {
     if (row >= rows) return;
@@ -44,7 +44,7 @@ gate_fwd_fp8_kernel(const MetaHeader* hdr, const uint8_t* __restrict__ row_type,
   load_row(row);
   for (; row < rows; row += step) {
     float x[C][4];
-    Raw<__nv_bfloat16> uu[C];
+    Raw<__nv_bfloat16, true> uu[C];
     const int type = type_next;
 #pragma unroll
     for (int i = 0; i < C; ++i)

@@ -628,7 +628,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 #pragma unroll 1
             for (int i0 = 0; i0 < 8; i0 += 4) {
               const int r0 = 16 * i0 + (tid >> 3), c = col + (tid & 7) * 4;
-              Raw<OT> res[4];
+              Raw<OT, true> res[4];
               if (p.epi.res) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {

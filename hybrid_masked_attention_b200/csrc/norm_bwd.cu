@@ -30,13 +30,12 @@ struct BwdArgs {
   float* partials;
 };
 
-__device__ __forceinline__ void unpack2(const Raw<float>& r, float2 (&v)[2]) {
-  v[0] = make_float2(r.v.x, r.v.y);
-  v[1] = make_float2(r.v.z, r.v.w);
-}
-__device__ __forceinline__ void unpack2(const Raw<__nv_bfloat16>& r, float2 (&v)[2]) {
-  v[0] = make_float2(__uint_as_float(r.v.x << 16), __uint_as_float(r.v.x & 0xffff0000u));
-  v[1] = make_float2(__uint_as_float(r.v.y << 16), __uint_as_float(r.v.y & 0xffff0000u));
+template <typename R>
+__device__ __forceinline__ void unpack2(const R& r, float2 (&v)[2]) {
+  float t[4];
+  unpack(r, t);
+  v[0] = make_float2(t[0], t[1]);
+  v[1] = make_float2(t[2], t[3]);
 }
 
 // C groups a warp: 4 with the next row's loads in flight (blocks of 8 warps, rows of up to
@@ -63,9 +62,9 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
   float2 dw[C][2];
 #pragma unroll
   for (int i = 0; i < C; ++i) dw[i][0] = dw[i][1] = make_float2(0.f, 0.f);
-  Raw<XT> xr[C];
-  Raw<YT> yr[C];
-  Raw<RRaw> rr[C];
+  Raw<XT, VEC> xr[C];
+  Raw<YT, VEC> yr[C];
+  Raw<RRaw, VEC> rr[C];
   float r_next = 0.f;
   auto load_row = [&](int64_t row) {
     if (row >= p.rows) return;
@@ -99,7 +98,7 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
     float2 xv[C][2], gv[C][2];
     const float2 r2 = make_float2(r, r);
     float2 s2 = make_float2(0.f, 0.f);
-    Raw<RRaw> res[C];
+    Raw<RRaw, VEC> res[C];
     float s = 0.f;
     if (live) {
 #pragma unroll
@@ -110,7 +109,7 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
           unpack2(yr[i], gv[i]);
           res[i] = rr[i];
           float2 ww[2];
-          unpack2(load_raw<VEC>(p.w + col0 + i * kGroup, lane, n), ww);
+          unpack2(load_const<VEC>(p.w + col0 + i * kGroup, lane, n), ww);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {  // two columns an instruction
             dw[i][j] = __ffma2_rn(gv[i][j], __fmul2_rn(xv[i][j], r2), dw[i][j]);

@@ -8,8 +8,7 @@
 // instruction and nothing goes through shared memory for the scales.
 //
 // Up to 1024 columns a warp holds its whole row (C groups); wider rows are split over W warps,
-// which exchange one partial sum.  Warps stride over the rows and load the next row before
-// they reduce the present one, so that loads are in flight throughout.
+// which exchange one partial sum.  Warps stride over the rows.
 #include <algorithm>
 #include <type_traits>
 
@@ -61,8 +60,8 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
   pdl_wait();
   pdl_trigger();
   if (p.err && *p.err) return;
-  Raw<XT> xr[C];
-  Raw<DRaw> dr[C];
+  Raw<XT, VEC> xr[C];
+  Raw<DRaw, VEC> dr[C];
   auto load_row = [&](int64_t row) {
     if (row >= p.rows) return;
     int64_t src = row;
@@ -78,12 +77,26 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
         if (n0 - i * kGroup > 0) dr[i] = load_raw<VEC>(pd + i * kGroup, lane, n0 - i * kGroup);
     }
   };
+  // Whether the next row is loaded before the present one is reduced, and whether the weight is
+  // held in registers: as measured.  The first helps by up to a quarter (53133 x 512 fp32: 29 to
+  // 24 us), but with a delta several instances then take twice as long (40000 x 1000, fp32 and an
+  // fp32 delta: 84 us without, 236 with), whichever way the loads are written; bf16 rows split over
+  // warps are the exception (8192 x 4096: 44 us with, 55 without; fp32 rows 94 and 66).
+  constexpr bool kAhead = !kDelta || (MULTI && C == 4 && VEC && sizeof(XT) == 2);
+  constexpr bool kHoldW = !MULTI;
+  const float* pw = p.w + col0;
+  Raw<float, VEC> wr[kHoldW ? C : 1];
+  if constexpr (kHoldW) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) wr[i] = load_const<VEC>(pw + i * kGroup, lane, n0 - i * kGroup);
+  }
   const int64_t step = (int64_t)gridDim.x * R;
   int64_t row = (int64_t)blockIdx.x * R + slot;
-  load_row(row);
+  if (kAhead) load_row(row);
   int flip = 0;
   // every warp of a block makes the same number of rounds (the barrier below)
   for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < p.rows; row0 += step, row += step, flip ^= 1) {
+    if (!kAhead) load_row(row);
     float h[C][4];
     float s = 0.f;
 #pragma unroll
@@ -100,7 +113,7 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
         for (int j = 0; j < 4; ++j) s = fmaf(h[i][j], h[i][j], s);
       }
     }
-    load_row(row + step);
+    if (kAhead) load_row(row + step);
     s = warp_sum32(s);
     if (MULTI) {
       if (lane == 0) s_part[flip][warp] = s;
@@ -112,7 +125,6 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
     if (p.rstd && sub == 0 && lane == 0) p.rstd[row] = r;
     uint8_t* qr = p.out.q + row * p.out.ld + col0;
     XT* xo = p.x_out + row * p.ld_xout + col0;
-    const float* pw = p.w + col0;
     float mine = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -120,7 +132,8 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
       if (n > 0) {
         if (kDelta && p.x_out) put4<VEC>(xo + i * kGroup, lane, n, h[i]);
         float ww[4], v[4];
-        load4<VEC>(pw + i * kGroup, lane, n, ww);
+        if constexpr (kHoldW) unpack(wr[i], ww);
+        else unpack(load_const<VEC>(pw + i * kGroup, lane, n), ww);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = h[i][j] * r * ww[j];
         const float m = quant_group<VEC>(v, lane, n, qr + i * kGroup);
@@ -153,8 +166,8 @@ inline int pow2_ceil(int v) {
   return p;
 }
 
-// Element-wise rows (VEC false) are held in the largest fitting of fewer variants: their
-// accesses, not their registers, are what they spend time on.
+// Element-wise rows (VEC false) of more than two groups go to the split form at once: eight groups
+// are 64 single loads a lane.
 template <typename XT, typename DT, bool VEC>
 cudaError_t shape(NormArgs<XT, DT>& a, cudaStream_t st) {
   const int G = (a.dim + kGroup - 1) / kGroup;
@@ -163,10 +176,10 @@ cudaError_t shape(NormArgs<XT, DT>& a, cudaStream_t st) {
   if constexpr (VEC) {
     if (G <= 4) return go<XT, DT, 4, false, VEC>(a, st);
     if (G <= 6) return go<XT, DT, 6, false, VEC>(a, st);
+    if (G <= 8) return go<XT, DT, 8, false, VEC>(a, st);
   }
-  if (G <= 8) return go<XT, DT, 8, false, VEC>(a, st);
   if (G <= 32) {
-    a.W = pow2_ceil((G + 3) / 4);
+    a.W = std::max(2, pow2_ceil((G + 3) / 4));
     return go<XT, DT, 4, true, VEC>(a, st);
   }
   a.W = pow2_ceil((G + 7) / 8);

@@ -21,7 +21,7 @@ quant_rows_kernel(int rows, int cols, int parts, int step_rows, int step_parts, 
   const int64_t unit = (int64_t)blockIdx.x * 8 + warp_index();
   int64_t row = unit / parts;
   int part = (int)(unit % parts);
-  Raw<T> next[kPer];
+  Raw<T, VEC> next[kPer];
   auto load_unit = [&](int64_t r, int c0) {
     if (r >= rows) return;
     const T* xr = x + r * ldx + c0;
