@@ -38,8 +38,21 @@ __device__ __forceinline__ void unpack2(const R& r, float2 (&v)[2]) {
   v[1] = make_float2(t[2], t[3]);
 }
 
+template <bool VEC>
+__device__ __forceinline__ void load_shared(const float* p, int lane, int n, float (&v)[4]) {
+  if (VEC) {
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (4 * lane < n) t = *reinterpret_cast<const float4*>(p + 4 * lane);
+    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = lane + 32 * j < n ? p[lane + 32 * j] : 0.f;
+  }
+}
+
 // C groups a warp: 4 with the next row's loads in flight (blocks of 8 warps, rows of up to
-// 4096 columns), 8 without (16 warps, 16384 columns; 128 registers do not hold a second row).
+// 4096 columns), 8 without (16 warps, 16384 columns; 128 registers hold neither a second row nor dw,
+// which is kept in shared memory: 2000 x 16384 bf16, 86 us).
 template <int C>
 constexpr int kThreadsB = C == 8 ? 512 : 256;
 
@@ -48,9 +61,12 @@ __global__ void __launch_bounds__(kThreadsB<C>, C == 8 ? 1 : 2)
 rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
   constexpr bool kRes = !std::is_same<RT, None>::value;
   constexpr bool kAhead = C < 8;
+  constexpr bool kResEarly = kAhead || VEC;  // dres is fetched with x and dy, not where it is added
+  constexpr bool kDwShared = C == 8;  // dw of a thread's 32 columns in shared memory instead of registers
   constexpr int kWarps = kThreadsB<C> / 32;
   using RRaw = typename std::conditional<kRes, RT, XT>::type;
-  extern __shared__ float s_dw[];  // [rows of a block - 1][dim]
+  // [rows of a block - 1][dim], to join dw at the end; kDwShared: [rows of a block][dim], the sums
+  extern __shared__ __align__(16) float s_dw[];
   __shared__ __align__(16) float s_part[2][kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int W = p.W, sub = warp % W, slot = warp / W, R = kWarps / W;
@@ -59,9 +75,17 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
   pdl_wait();
   pdl_trigger();
   const float inv_dim = 1.f / (float)p.dim;
-  float2 dw[C][2];
+  float2 dw[kDwShared ? 1 : C][2];
+  if constexpr (kDwShared) {  // (every element belongs to one thread)
 #pragma unroll
-  for (int i = 0; i < C; ++i) dw[i][0] = dw[i][1] = make_float2(0.f, 0.f);
+    for (int i = 0; i < C; ++i) {
+      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+      put4<VEC>(s_dw + slot * p.dim + col0 + i * kGroup, lane, n0 - i * kGroup, zero);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; ++i) dw[i][0] = dw[i][1] = make_float2(0.f, 0.f);
+  }
   Raw<XT, VEC> xr[C];
   Raw<YT, VEC> yr[C];
   Raw<RRaw, VEC> rr[C];
@@ -72,18 +96,14 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
     const XT* px = p.x + row * p.ldx + col0;
     const YT* py = p.dy + row * p.ld_dy + col0;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int n = n0 - i * kGroup;
-      if (n > 0) {
-        xr[i] = load_raw<VEC>(px + i * kGroup, lane, n);
-        yr[i] = load_raw<VEC>(py + i * kGroup, lane, n);
-      }
+    for (int i = 0; i < C; ++i) {  // (a group past the row loads nothing, and holds zeros: norm_fp8.cu)
+      xr[i] = load_raw<VEC>(px + i * kGroup, lane, n0 - i * kGroup);
+      yr[i] = load_raw<VEC>(py + i * kGroup, lane, n0 - i * kGroup);
     }
-    if constexpr (kRes && kAhead) {
+    if constexpr (kRes && kResEarly) {
       const RT* pr = p.dres + row * p.ld_dres + col0;
 #pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (n0 - i * kGroup > 0) rr[i] = load_raw<VEC>(pr + i * kGroup, lane, n0 - i * kGroup);
+      for (int i = 0; i < C; ++i) rr[i] = load_raw<VEC>(pr + i * kGroup, lane, n0 - i * kGroup);
     }
   };
   const int64_t step = (int64_t)gridDim.x * R;
@@ -104,18 +124,28 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const int n = n0 - i * kGroup;
-        if (n > 0) {
-          unpack2(xr[i], xv[i]);
-          unpack2(yr[i], gv[i]);
-          res[i] = rr[i];
-          float2 ww[2];
-          unpack2(load_const<VEC>(p.w + col0 + i * kGroup, lane, n), ww);
+        unpack2(xr[i], xv[i]);
+        unpack2(yr[i], gv[i]);
+        res[i] = rr[i];
+        float2 ww[2], part[2];
+        float* sd = s_dw + slot * p.dim + col0 + i * kGroup;
+        if constexpr (kDwShared) {
+          float t[4];
+          load_shared<VEC>(sd, lane, n, t);
+          part[0] = make_float2(t[0], t[1]);
+          part[1] = make_float2(t[2], t[3]);
+        }
+        unpack2(load_const<VEC>(p.w + col0 + i * kGroup, lane, n), ww);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {  // two columns an instruction
-            dw[i][j] = __ffma2_rn(gv[i][j], __fmul2_rn(xv[i][j], r2), dw[i][j]);
-            gv[i][j] = __fmul2_rn(gv[i][j], ww[j]);
-            s2 = __ffma2_rn(gv[i][j], xv[i][j], s2);
-          }
+        for (int j = 0; j < 2; ++j) {  // two columns an instruction
+          if constexpr (!kDwShared) dw[i][j] = __ffma2_rn(gv[i][j], __fmul2_rn(xv[i][j], r2), dw[i][j]);
+          else part[j] = __ffma2_rn(gv[i][j], __fmul2_rn(xv[i][j], r2), part[j]);
+          gv[i][j] = __fmul2_rn(gv[i][j], ww[j]);
+          s2 = __ffma2_rn(gv[i][j], xv[i][j], s2);
+        }
+        if constexpr (kDwShared) {
+          const float t[4] = {part[0].x, part[0].y, part[1].x, part[1].y};
+          put4<VEC>(sd, lane, n, t);
         }
       }
     }
@@ -139,7 +169,7 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
           for (int j = 0; j < 2; ++j) o[j] = __fmul2_rn(r2, __ffma2_rn(xv[i][j], c2, gv[i][j]));
           if constexpr (kRes) {
             float2 t[2];
-            if constexpr (kAhead) unpack2(res[i], t);
+            if constexpr (kResEarly) unpack2(res[i], t);
             else unpack2(load_raw<VEC>(p.dres + row * p.ld_dres + col0 + i * kGroup, lane, n), t);
 #pragma unroll
             for (int j = 0; j < 2; ++j) o[j] = __fadd2_rn(o[j], t[j]);
@@ -151,31 +181,33 @@ rmsnorm_bwd_kernel(const __grid_constant__ BwdArgs<XT, YT, RT> p) {
     }
   }
   // the block's partial row: slots 1.. hand theirs over through shared memory
-  if (R > 1) {
+  if constexpr (kDwShared) {
+    if (R > 1) __syncthreads();
+  } else if (R > 1) {
     if (slot > 0)
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
+      for (int i = 0; i < C; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int c = col0 + i * kGroup + lane_col<VEC>(lane, j);
-            if (c < p.dim) s_dw[(size_t)(slot - 1) * p.dim + c] = j & 1 ? dw[i][j >> 1].y : dw[i][j >> 1].x;
-          }
-      }
+          const int c = col0 + i * kGroup + lane_col<VEC>(lane, j);
+          if (c < p.dim) s_dw[(size_t)(slot - 1) * p.dim + c] = j & 1 ? dw[i][j >> 1].y : dw[i][j >> 1].x;
+        }
     __syncthreads();
   }
   if (slot == 0)
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
+    for (int i = 0; i < C; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-          const int c = col0 + i * kGroup + lane_col<VEC>(lane, j);
-          if (c < p.dim) {
-            float t = j & 1 ? dw[i][j >> 1].y : dw[i][j >> 1].x;
-            for (int k = 0; k < R - 1; ++k) t += s_dw[(size_t)k * p.dim + c];
-            p.partials[(size_t)blockIdx.x * p.dim + c] = t;
-          }
+        const int c = col0 + i * kGroup + lane_col<VEC>(lane, j);
+        if (c < p.dim) {
+          float t;
+          if constexpr (kDwShared) t = s_dw[c];
+          else t = j & 1 ? dw[i][j >> 1].y : dw[i][j >> 1].x;
+          for (int k = kDwShared; k < R - !kDwShared; ++k) t += s_dw[(size_t)k * p.dim + c];
+          p.partials[(size_t)blockIdx.x * p.dim + c] = t;
         }
-    }
+      }
 }
 
 // dw = sum of the partial rows: 8 columns (one 32-byte sector) a block, 32 threads down each,
@@ -211,10 +243,16 @@ cudaError_t go(BwdArgs<XT, YT, RT>& a, float* dw, cudaStream_t st) {
   const int G = (a.dim + kGroup - 1) / kGroup;
   a.W = pow2_ceil((G + C - 1) / C);
   const int R = warps / a.W;
-  const size_t smem = sizeof(float) * (size_t)(R - 1) * a.dim;  // R W C 128 columns at most: under 33 KB
+  // C = 4: R W 512 columns, 4096 at most, less a row; C = 8: R W 1024, 16384 at most
+  const size_t smem = sizeof(float) * (size_t)(C == 8 ? R : R - 1) * a.dim;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(rmsnorm_bwd_kernel<XT, YT, RT, C, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+    if (e != cudaSuccess) return e;
+  }
   const int per_sm = C == 8 ? 1 : 2;  // the kernel's launch bound
   const int blocks = (int)std::min<int64_t>(std::min(kNormBwdBlocks, per_sm * sm_count()), ((int64_t)a.rows + R - 1) / R);
-  cudaError_t e = launch_pdl(rmsnorm_bwd_kernel<XT, YT, RT, C, VEC>, dim3(blocks), dim3(32 * warps), smem, st, a);
+  e = launch_pdl(rmsnorm_bwd_kernel<XT, YT, RT, C, VEC>, dim3(blocks), dim3(32 * warps), smem, st, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(dw_reduce_kernel, dim3((a.dim + 7) / 8), dim3(256), 0, st, (const float*)a.partials, blocks, a.dim, dw);
 }

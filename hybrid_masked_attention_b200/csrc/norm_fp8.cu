@@ -67,22 +67,23 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
     int64_t src = row;
     if constexpr (kMapped) src = row >= p.mapped ? (int64_t)p.row_map[row - p.mapped] : row;
     const XT* px = p.x + src * p.ldx + col0;
+    // No test of the group around a load or its use (past the row the lanes' own predicates load
+    // nothing, and zeros are held): where both stood under the same test, the compiler joined them
+    // in some instances and the row's loads were waited for one by one (40000 x 1000, fp32 and an
+    // fp32 delta: 236 us against 84).
 #pragma unroll
     for (int i = 0; i < C; ++i)
-      if (n0 - i * kGroup > 0) xr[i] = load_raw<VEC>(px + i * kGroup, lane, n0 - i * kGroup);
+      xr[i] = load_raw<VEC>(px + i * kGroup, lane, n0 - i * kGroup);
     if constexpr (kDelta) {
       const DT* pd = p.delta + row * p.ld_delta + col0;
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        if (n0 - i * kGroup > 0) dr[i] = load_raw<VEC>(pd + i * kGroup, lane, n0 - i * kGroup);
+        dr[i] = load_raw<VEC>(pd + i * kGroup, lane, n0 - i * kGroup);
     }
   };
-  // Whether the next row is loaded before the present one is reduced, and whether the weight is
-  // held in registers: as measured.  The first helps by up to a quarter (53133 x 512 fp32: 29 to
-  // 24 us), but with a delta several instances then take twice as long (40000 x 1000, fp32 and an
-  // fp32 delta: 84 us without, 236 with), whichever way the loads are written; bf16 rows split over
-  // warps are the exception (8192 x 4096: 44 us with, 55 without; fp32 rows 94 and 66).
-  constexpr bool kAhead = !kDelta || (MULTI && C == 4 && VEC && sizeof(XT) == 2);
+  // The next row is loaded before the present one is reduced, and one-warp rows hold the weight in
+  // registers.  (Groups of eight a warp of a split row leave no registers for either.)
+  constexpr bool kAhead = !(C == 8 && MULTI);
   constexpr bool kHoldW = !MULTI;
   const float* pw = p.w + col0;
   Raw<float, VEC> wr[kHoldW ? C : 1];
@@ -101,17 +102,15 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      if (n0 - i * kGroup > 0) {
-        unpack(xr[i], h[i]);
-        if constexpr (kDelta) {
-          float d[4];
-          unpack(dr[i], d);
+      unpack(xr[i], h[i]);
+      if constexpr (kDelta) {
+        float d[4];
+        unpack(dr[i], d);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) h[i][j] += d[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s = fmaf(h[i][j], h[i][j], s);
+        for (int j = 0; j < 4; ++j) h[i][j] += d[j];
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s = fmaf(h[i][j], h[i][j], s);
     }
     if (kAhead) load_row(row + step);
     s = warp_sum32(s);
