@@ -2,9 +2,9 @@
 // product: e4m3 values (4 exponent, 3 mantissa bits, largest 448) with one fp32 scale for
 // each group.  A group is 128 consecutive columns of one row, or a block of 128 x 128; the
 // last ones are ragged.  With m = max(max |v|, 2^-100) over the group
-//     scale = m / 448,   q = e4m3(v * (448 / m))   (round to nearest even, saturating),
-// so that v ~ scale * q with an error of at most half a step of e4m3 (2^-4 relative) for
-// |v| >= m * 2^-6 / 448 and of m * 2^-10 / 448 below that.  The floor keeps 448 / m finite
+//     scale = m / 448,   q = e4m3(v * (448 (1 / m)))   (round to nearest even, saturating),
+// every operation rounded to nearest fp32, so that v ~ scale * q with an error of at most half a step of e4m3 (2^-4 relative) for
+// |v| >= m * 2^-6 / 448 and of m * 2^-10 / 448 below that.  The floor keeps 1 / m finite
 // for a group of zeros (q = 0).  A NaN does not enter m; it stays a NaN of its own element.
 // An infinity makes the scale infinite, and the whole group reads back as NaN.
 #pragma once
@@ -183,15 +183,29 @@ __device__ __forceinline__ void put4_e4m3(uint8_t* p, int lane, int n, const flo
   }
 }
 
-// Quantises the warp's 128-column group (columns past n hold zeros), writes its bytes and
-// returns m = max(max |v|, 2^-100), from which the caller writes the scale m / 448.  448 / m is
-// 448 times an approximate reciprocal: 3 half steps of fp32 from the quotient, far below half a
-// step of e4m3, for a fifth of a division's instructions (of which a group would need 32 lanes').
-template <bool VEC>
-__device__ __forceinline__ float quant_group(const float (&v)[4], int lane, int n, uint8_t* q) {
-  const float m = fmaxf(warp_absmax(absmax4(v)), kAmaxFloor);
-  put4_e4m3<VEC>(q, lane, n, v, kE4m3Max * rcp_approx(m));
-  return m;
+// The factor of a group, 448 (1 / m): reciprocal and product each rounded to nearest, which is
+// what `448.0 / m` is in torch, so that the quantiser's bytes are those of the plain form.  (With
+// an approximate reciprocal one value in 10^5 or so fell on the other side of a rounding border.)
+__device__ __forceinline__ float quant_factor(float m) { return kE4m3Max * __frcp_rn(m); }
+
+// Quantises the warp's C neighbouring 128-column groups of a row, of which n columns are left
+// (columns past them hold zeros), and writes their bytes.  Lane i < C returns group i's m =
+// max(max |v|, 2^-100), from which the caller writes the scale m / 448.  Lane i also computes the
+// factor of group i: one reciprocal for the row instead of one a group.
+template <bool VEC, int C>
+__device__ __forceinline__ float quant_groups(const float (&v)[C][4], int lane, int n, uint8_t* q) {
+  float mine = kAmaxFloor;
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    if (i * kGroup < n) {
+      const float m = fmaxf(warp_absmax(absmax4(v[i])), kAmaxFloor);
+      if (lane == i) mine = m;
+    }
+  const float f = quant_factor(mine);
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    if (i * kGroup < n) put4_e4m3<VEC>(q + i * kGroup, lane, n - i * kGroup, v[i], __shfl_sync(0xffffffffu, f, i));
+  return mine;
 }
 
 // Matrices of the 8-bit entry points.  ld: row pitch in elements.

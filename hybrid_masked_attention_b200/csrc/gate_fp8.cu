@@ -84,17 +84,15 @@ gate_fwd_fp8_kernel(const MetaHeader* hdr, const uint8_t* __restrict__ row_type,
       if (lane == 0) *reinterpret_cast<float2*>(stats + 2 * row) = make_float2(mean, rstd);
     }
     uint8_t* q = out.q + row * out.ld;
-    float mine = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i)
       if (i < G) {
-        float v[4], t[4];
+        float t[4];
         unpack(uu[i], t);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = x[i][j] * t[j];
-        const float m = quant_group<true>(v, lane, D - i * kGroup, q + i * kGroup);
-        if (lane == i) mine = m;
+        for (int j = 0; j < 4; ++j) x[i][j] *= t[j];
       }
+    const float mine = quant_groups<true>(x, lane, D, q);
     if (lane < G) out.scale[row * out.ld_scale + lane] = mine / kE4m3Max;
   }
 }

@@ -125,21 +125,19 @@ add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs<XT, DT> p) {
     if (p.rstd && sub == 0 && lane == 0) p.rstd[row] = r;
     uint8_t* qr = p.out.q + row * p.out.ld + col0;
     XT* xo = p.x_out + row * p.ld_xout + col0;
-    float mine = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int n = n0 - i * kGroup;
       if (n > 0) {
         if (kDelta && p.x_out) put4<VEC>(xo + i * kGroup, lane, n, h[i]);
-        float ww[4], v[4];
+        float ww[4];
         if constexpr (kHoldW) unpack(wr[i], ww);
         else unpack(load_const<VEC>(pw + i * kGroup, lane, n), ww);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = h[i][j] * r * ww[j];
-        const float m = quant_group<VEC>(v, lane, n, qr + i * kGroup);
-        if (lane == i) mine = m;
+        for (int j = 0; j < 4; ++j) h[i][j] = h[i][j] * r * ww[j];
       }
     }
+    const float mine = quant_groups<VEC>(h, lane, n0, qr);
     if (lane < C && n0 > lane * kGroup) p.out.scale[row * p.out.ld_scale + sub * C + lane] = mine / kE4m3Max;
   }
 }

@@ -44,13 +44,7 @@ quant_rows_kernel(int rows, int cols, int parts, int step_rows, int step_parts, 
       ++row;
     }
     load_unit(row, part * kPer * kGroup);
-    float mine = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (c0 + i * kGroup < cols) {
-        const float m = quant_group<VEC>(v[i], lane, cols - c0 - i * kGroup, q + i * kGroup);
-        if (lane == i) mine = m;
-      }
+    const float mine = quant_groups<VEC>(v, lane, cols - c0, q);
     if (lane < kPer && c0 + lane * kGroup < cols) s[lane] = mine / kE4m3Max;
   }
 }
@@ -83,11 +77,11 @@ quant_blocks_kernel(int rows, int cols, int G, const T* __restrict__ x, int64_t 
   m = kAmaxFloor;
 #pragma unroll
   for (int k = 0; k < 8; ++k) m = fmaxf(m, s_max[k]);
-  const float inv = kE4m3Max * rcp_approx(m);  // as quant_group
+  const float f = quant_factor(m);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int64_t row = r0 + warp + 8 * i;
-    if (row < rows) put4_e4m3<VEC>(out.q + row * out.ld + c0, lane, n, v[i], inv);
+    if (row < rows) put4_e4m3<VEC>(out.q + row * out.ld + c0, lane, n, v[i], f);
   }
   if (threadIdx.x == 0) out.scale[rb * out.ld_scale + g] = m / kE4m3Max;
 }

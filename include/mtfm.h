@@ -412,7 +412,7 @@ mtfm_status mtfm_v2_target_layer_fwd(const mtfm_cfg* cfg, const void* d_meta, in
  * (activations: scale [rows, ceil(cols / 128)]) or a block of 128 x 128
  * (weights: scale [ceil(rows / 128), ceil(cols / 128)]); the last groups are
  * ragged.  With m = max(max |v|, 2^-100) over the group
- *     scale = m / 448,   q = e4m3(v * (448 / m))   (nearest even, saturating)
+ *     scale = m / 448,   q = e4m3(v * f),   f = 448 (1 / m)   (nearest even, saturating)
  * and v ~ scale * q.  A NaN stays a NaN of its own element and does not enter m;
  * an infinity makes its group's scale infinite (the group reads back as NaN).
  *
