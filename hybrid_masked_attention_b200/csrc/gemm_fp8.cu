@@ -156,7 +156,7 @@ template <typename OT>
 __device__ __forceinline__ void act32(const Args& p, float (&v)[32]) {
   if (p.epi.act == MTFM_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) silu_pair<OT>(v[j], v[j + 1]);
+    for (int j = 0; j < 32; j += 4) silu_4<OT>(v, j);
   }
 }
 // The residual of a row whose 32 columns start at col.

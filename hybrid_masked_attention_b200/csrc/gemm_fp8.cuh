@@ -55,29 +55,44 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// SiLU of two values, for fp32 outputs: x / (1 + exp(-x)) with one reciprocal for both, 1/a =
-// b / (a b).  The exponentials are held below 2^63 (x > -43.6) so that a b stays finite; beyond
-// that |SiLU| < 5e-18 is off by no more than that.  Otherwise within a few roundings of fp32.
-__device__ __forceinline__ void silu2(float& x0, float& x1) {
-  const float a = 1.f + fminf(ex2_approx(x0 * -kLog2E), 0x1p63f), b = 1.f + fminf(ex2_approx(x1 * -kLog2E), 0x1p63f);
-  const float r = rcp_approx(a * b);
-  x0 = x0 * (r * b);
-  x1 = x1 * (r * a);
+// SiLU without a cancellation at either end: with e = exp(-|x|) in [0, 1],
+//   SiLU(x) = x / (1 + e) for x >= 0,  x e / (1 + e) below.
+// Relative error at most (13 + 2 |x|) 2^-24 (the exponential's argument is rounded twice, 2 |x|;
+// exponential 4, four shared reciprocals 7, products 2); results below 2^-119 in magnitude are 0.
+// NaN gives NaN, and so does minus infinity (0 times infinity).
+__device__ __forceinline__ float silu_exp(float x) { return ex2_approx(-fabsf(x * kLog2E)); }
+__device__ __forceinline__ float silu_top(float x, float e) { return x < 0.f ? x * e : x; }
+__device__ __forceinline__ float silu1(float x) {
+  const float e = silu_exp(x);
+  return silu_top(x, e) * rcp_approx(1.f + e);
+}
+// Four values with one reciprocal, 1/a = (b c d) / (a b c d): 1.25 special-function operations a
+// value.  The denominators lie in [1, 2]; a NaN's is taken as 2, which keeps it out of the others.
+__device__ __forceinline__ void silu4(float2& x, float2& y) {
+  const float e0 = silu_exp(x.x), e1 = silu_exp(x.y), e2 = silu_exp(y.x), e3 = silu_exp(y.y);
+  const float a = fminf(1.f + e0, 2.f), b = fminf(1.f + e1, 2.f), c = fminf(1.f + e2, 2.f), d = fminf(1.f + e3, 2.f);
+  const float ab = a * b, cd = c * d, r = rcp_approx(ab * cd);
+  const float rab = r * cd, rcd = r * ab;
+  x = __fmul2_rn(make_float2(silu_top(x.x, e0), silu_top(x.y, e1)), __fmul2_rn(make_float2(rab, rab), make_float2(b, a)));
+  y = __fmul2_rn(make_float2(silu_top(y.x, e2), silu_top(y.y, e3)), __fmul2_rn(make_float2(rcd, rcd), make_float2(d, c)));
 }
 // For bf16 outputs: h + h tanh(h), h = x / 2, with the hardware's tanh (one special-function
-// operation instead of 1.5, and half the instructions; they bound a K = 512 projection:
-// 53133 x 1280 takes 72 us with silu2 and 62 with this).  tanh's relative error of 2^-11 makes an
+// operation, and fewer instructions; they bound a K = 512 projection).  tanh's relative error of 2^-11 makes an
 // error of at most 2^-12 |x|, a sixteenth of bf16's half step at |x|: phi_1 of the bf16
 // projections (gemm_tc.cu) is the same function.
 template <typename OT>
-__device__ __forceinline__ void silu_pair(float& x0, float& x1) {
+__device__ __forceinline__ void silu_4(float (&v)[32], int j) {
   if constexpr (sizeof(OT) == 2) {
-    x0 = silu_fast(x0);
-    x1 = silu_fast(x1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[j + i] = silu_fast(v[j + i]);
   } else {
-    silu2(x0, x1);
+    float2 x = make_float2(v[j], v[j + 1]), y = make_float2(v[j + 2], v[j + 3]);
+    silu4(x, y);
+    v[j] = x.x, v[j + 1] = x.y, v[j + 2] = y.x, v[j + 3] = y.y;
   }
 }
+template <typename OT>
+__device__ __forceinline__ float silu_one(float x) { return sizeof(OT) == 2 ? silu_fast(x) : silu1(x); }
 
 // ---------------------------------------------------------------- host
 // Row-major e4m3 matrix [rows, cols], row pitch ld bytes; boxes of box_rows x 128 columns.
