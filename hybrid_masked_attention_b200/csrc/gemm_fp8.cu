@@ -152,11 +152,14 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       : "memory");
 }
 
-template <typename OT>
 __device__ __forceinline__ void act32(const Args& p, float (&v)[32]) {
   if (p.epi.act == MTFM_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) silu_4<OT>(v, j);
+    for (int j = 0; j < 32; j += 4) {
+      float2 x = make_float2(v[j], v[j + 1]), y = make_float2(v[j + 2], v[j + 3]);
+      silu4(x, y);
+      v[j] = x.x, v[j + 1] = x.y, v[j + 2] = y.x, v[j + 3] = y.y;
+    }
   }
 }
 // The residual of a row whose 32 columns start at col.
@@ -548,7 +551,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             float v[32];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[2 * j] = acc[wc / 2 + j].x, v[2 * j + 1] = acc[wc / 2 + j].y;
-            act32<OT>(p, v);
+            act32(p, v);
 #pragma unroll
             for (int i = 0; i < 2 * (int)sizeof(OT); ++i) {
               uint4* at = reinterpret_cast<uint4*>(rowp + (((c * 2 * (int)sizeof(OT) + i) ^ (r_in & 7)) << 4));
@@ -596,7 +599,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             float v[32];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[2 * j] = acc[wc / 2 + j].x, v[2 * j + 1] = acc[wc / 2 + j].y;
-            act32<OT>(p, v);
+            act32(p, v);
 #pragma unroll
             for (int i = 0; i < 2 * (int)sizeof(BT); ++i) {
               const int chunk = c * 2 * (int)sizeof(BT) + i;
@@ -666,7 +669,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             float v[32];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[2 * j] = acc[c * 16 + j].x, v[2 * j + 1] = acc[c * 16 + j].y;
-            act32<OT>(p, v);
+            act32(p, v);
             residual32<OT>(p, orow(row), col0 + c * 32, v);
             store32<OT>(p, orow(row), col0 + c * 32, v);
           }

@@ -267,7 +267,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_cons
           c0 = e.seg_begin[q];
         }
       auto finish = [&](int m, float v) {
-        if (e.act == MTFM_ACT_SILU) v = silu_one<OT>(v);
+        if (e.act == MTFM_ACT_SILU) v = silu1(v);
         const int64_t orow = e.row_map ? e.row_map[m] : m;
         if (e.res) v += (float)static_cast<const OT*>(e.res)[orow * e.ld_res + col];
         base[orow * ld + (col - c0)] = (OT)v;

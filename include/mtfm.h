@@ -470,8 +470,8 @@ mtfm_status mtfm_fp8_quant(int32_t rows, int32_t cols, const void* d_x, int32_t 
  * 1 x 128 groups and B [n, k] in 128 x 128 blocks (a weight, "out x in"; the gradient
  * dX = dY W is the same call on quantised dY and on the quantised transpose of W).
  * Products of one 128-deep block are summed by the tensor cores, scaled, and added in fp32.
- * act: MTFM_ACT_SILU for fp32 outputs to a relative (13 + 2 |x|) 2^-24 (results below 2^-119
- * in magnitude may be 0; NaN and minus infinity give NaN); for bf16 outputs with the hardware's tanh (an error of at most 2^-12 |x|, as in the bf16 stack), then rounded to nearest.
+ * act: MTFM_ACT_SILU to a relative (13 + 2 |x|) 2^-24 before the output's rounding (results
+ * below 2^-119 in magnitude may be 0; NaN and minus infinity give NaN).
  * A and B: 16-byte aligned, pitches multiples of 16 (a single row may have any pitch).
  * out, res: out_type; res may be NULL, or out itself.  k >= 1.
  * d_status: device word, zeroed once by the caller; a call on a word that is not zero does

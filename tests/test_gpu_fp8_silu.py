@@ -56,7 +56,7 @@ def check(out, x):
 
 # rows of A up to 32, or CTA pairs; columns that leave by TMA, or directly
 @pytest.mark.parametrize("n", [8, 7, 264])
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_silu_over_the_range(n, dtype, cuda_ok):
     x = arguments()
     check(*product(x, n, dtype))
@@ -65,7 +65,7 @@ def test_silu_over_the_range(n, dtype, cuda_ok):
 
 
 @pytest.mark.parametrize("rows", [3, 200])
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_silu_of_nan_and_infinity(rows, dtype, cuda_ok):
     """Infinity stays, minus infinity is 0 times infinity, NaN stays in its own element."""
     x = torch.full((rows,), 1.5, device="cuda")
