@@ -247,7 +247,9 @@ cudaError_t go(BwdArgs<XT, YT, RT>& a, float* dw, cudaStream_t st) {
   // C = 4: R W 512 columns, 4096 at most, less a row; C = 8: R W 1024, 16384 at most
   const size_t smem = sizeof(float) * (size_t)(C == 8 ? R : R - 1) * a.dim;
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) {
+  // C = 8 always: what a block may have without the attribute, 48 KB, counts s_part too (with the
+  // test on `smem` alone, dims 6129..6144 and 12257..12288 were refused at their launch)
+  if constexpr (C == 8) {
     e = cudaFuncSetAttribute(rmsnorm_bwd_kernel<XT, YT, RT, C, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
     if (e != cudaSuccess) return e;
   }
