@@ -31,7 +31,8 @@
 //
 // Every wait is bounded; a wait that gives up raises its CTA's abort flag, the other CTA's own
 // waits then run out too, both meet at the cluster barrier, and the error word gets the
-// timeout bit.
+// timeout bit.  The epilogue's barriers within a warpgroup have no limit: its warps leave their
+// tiles together (gemm_fp8_flow.cuh).
 #include <cuda.h>
 
 #include <algorithm>
@@ -39,6 +40,7 @@
 #include <type_traits>
 
 #include "gemm_fp8.cuh"
+#include "gemm_fp8_flow.cuh"
 
 namespace mtfm {
 namespace {
@@ -230,6 +232,15 @@ __device__ __forceinline__ void store32(const Args& p, int64_t orow, int col, co
   }
 }
 
+// A barrier of the warpgroup (waits without a limit: every warp has to come, gemm_fp8_flow.cuh),
+// and one that says whether `ok` holds in all of its threads.
+__device__ __forceinline__ bool wg_vote(int id, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.and.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(all) : "r"((uint32_t)ok), "r"(id) : "memory");
+  return all != 0;
+}
 __device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // 4-byte asynchronous copy global -> shared, zero-filled past `bytes`; and an arrival on an
@@ -458,7 +469,6 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     const uint32_t b_res = smem_addr(&bars.res_full[wg]);
     uint32_t res_issued = 0, ph_res = 0;
     auto orow = [&](int m) { return (int64_t)(p.epi.row_map ? p.epi.row_map[m] : m); };
-    bool ok = true;
     uint32_t n = (uint32_t)(set * nK);  // blocks before this set's next one: buffer n % kAcc
     uint32_t phases = 0;                // of this set's barriers, one bit a buffer
     const uint32_t scf0 = b_scf + (uint32_t)((kParts > 1 ? 0 : set) * kSlots) * 8;
@@ -467,24 +477,25 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     uint32_t sc_phases = 0;
     float sc = 0.f;  // sa sb of this thread's row and columns for the next block
     auto next_scale = [&]() {
-      const bool got = __all_sync(0xffffffffu, mbar_wait(scf0 + (uint32_t)slot * 8, (sc_phases >> slot) & 1, abort_flag));
+      __all_sync(0xffffffffu, mbar_wait(scf0 + (uint32_t)slot * 8, (sc_phases >> slot) & 1, abort_flag));
       sc = s_scale[slot * 128 + r_in] * *const_cast<const volatile float*>(&bars.sb[slot][part]);
       sc_phases ^= 1u << slot;
       __syncwarp();
       if (lane == 0) mbar_arrive(b_sce + (uint32_t)slot * 8);
       slot = slot + 1 == kSlots ? 0 : slot + 1;
-      return got;
     };
+    // A warp's way through the tiles is epilogue_tiles() below.
     // BN = 256: a tile's first scale is fetched in the last block of the one before.  With sets it
     // is fetched when the tile begins: a set that waited for it while it holds a TMEM buffer would
     // wait for the other set's tile, which needs that buffer.
-    if (kSets == 1 && first < n_tiles) ok = next_scale();
-    for (int t = first + set * step; ok && t < n_tiles; t += kSets * step, n += (uint32_t)((kSets - 1) * nK), slot = (slot + (kSets - 1) * nK) % kSlots) {
+    float2 acc[kCols / 2];
+    int m0 = 0, col0 = 0;  // of the tile
+    auto begin = [&](int t) {
       const Tile tl = tile_at<BN>(p, t, nM, nN);
-      const int m0 = tl.m0 + (int)rank * kBM;
-      const int row = m0 + r_in;
-      const int col0 = tl.n0 + tcol;
-      if (OUT == kOutTmaRes && issuer) {
+      m0 = tl.m0 + (int)rank * kBM;
+      col0 = tl.n0 + tcol;
+      // (after a wait that gave up the barrier may be half done: not armed again)
+      if (OUT == kOutTmaRes && issuer && *abort_flag == 0) {
         bulk_wait_read<0>();  // the last tile's stores have read the staging
         mbar_expect_tx(b_res, kResBytes);
 #pragma unroll
@@ -493,20 +504,14 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             tma_load_2d(sstage + b * kBoxBytes, &tm_o1, b_res, col0 + b * kOutCols, m0);
         ++res_issued;
       }
-      float2 acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-      if (kSets > 1) {
-        ok = next_scale();
-        if (!ok) break;
-      }
+    };
+    auto blocks = [&](int t) {
       for (int kb = 0; kb < nK; ++kb, ++n) {
         const float2 s2 = make_float2(sc, sc);
         const int a = (int)(n % kAcc);
-        if (!__all_sync(0xffffffffu, mbar_wait(accf0 + (uint32_t)a * 8, (phases >> a) & 1, abort_flag))) {
-          ok = false;
-          break;
-        }
+        if (!__all_sync(0xffffffffu, mbar_wait(accf0 + (uint32_t)a * 8, (phases >> a) & 1, abort_flag))) return;
         phases ^= 1u << a;
         tc_fence_after();
         const uint32_t ta = tlane + (uint32_t)(a * 128);
@@ -515,7 +520,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           uint32_t raw[32];
           tmem_ld32(ta + (uint32_t)(c * 32), raw);
           if (c == 0) {  // the next block's scale is fetched while this one is on its way from TMEM
-            if (kb + 1 < nK || (kSets == 1 && t + step < n_tiles)) ok = next_scale();
+            if (kb + 1 < nK || (kSets == 1 && t + step < n_tiles)) next_scale();
           }
           tmem_ld_wait();
           if (c + 1 == kCols / 32) {
@@ -529,18 +534,14 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                                          acc[c * 16 + j]);
         }
       }
-      if (OUT != kOutDirect) {
-        // uniform over the warpgroup before its barriers
-        uint32_t all;
-        asm volatile(
-            "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.and.pred q, %2, 128, p; selp.u32 %0, 1, 0, q; }"
-            : "=r"(all) : "r"((uint32_t)ok), "r"(bar_id) : "memory");
-        ok = all != 0;
-      }
-      if (!ok) break;
+    };
+    auto vote = [&]() {
+      if constexpr (OUT == kOutDirect) return (bool)__all_sync(0xffffffffu, *abort_flag == 0);  // no barriers: by warps
+      else return wg_vote(bar_id, *abort_flag == 0);
+    };
+    auto finish = [&](int) {
       if constexpr (OUT == kOutTmaRes) {
-        // (a wait that gives up leaves the warpgroup's barriers below whole: every warp goes on)
-        ok = mbar_wait(b_res, ph_res, abort_flag);
+        mbar_wait(b_res, ph_res, abort_flag);
         ph_res ^= 1;
 #pragma unroll
         for (int b = 0; b < kResBoxes; ++b) {
@@ -574,14 +575,14 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         }
         fence_proxy_async();
         wg_sync(bar_id);
-        if (issuer && ok && m0 < p.M) {
+        // (after a wait that gave up the staging may hold no sums; the barrier orders the flag)
+        if (issuer && *abort_flag == 0 && m0 < p.M) {
 #pragma unroll
           for (int b = 0; b < kResBoxes; ++b)
             if (col0 + b * kOutCols < p.N && store_ok(p.err, col0 + b * kOutCols, p.N, (int)sizeof(OT), m0, p.M))
               tma_store_2d(&tm_o0, sstage + b * kBoxBytes, col0 + b * kOutCols, m0);
           bulk_commit();
         }
-        ok = __all_sync(0xffffffffu, ok);
       } else if constexpr (OUT != kOutDirect) {
         using BT = typename std::conditional<OUT == kOutTma, OT, float>::type;  // staged before a residual: unrounded
         constexpr int kBoxCols = 128 / (int)sizeof(BT);  // 64 bf16 or 32 fp32
@@ -662,7 +663,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             }
           }
         }
-      } else if (row < p.M) {
+      } else if (const int row = m0 + r_in; row < p.M) {
 #pragma unroll
         for (int c = 0; c < kCols / 32; ++c) {
           if (col0 + c * 32 < p.N) {
@@ -675,7 +676,12 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           }
         }
       }
-    }
+    };
+    auto next = [&]() {  // past the other sets' blocks
+      n += (uint32_t)((kSets - 1) * nK);
+      slot = (slot + (kSets - 1) * nK) % kSlots;
+    };
+    epilogue_tiles<kSets == 1>(first + set * step, n_tiles, kSets * step, next_scale, begin, blocks, vote, finish, next);
     if (issuer) {
       if (OUT == kOutTma || OUT == kOutTmaRes) bulk_wait<0>();  // every store has completed before the CTA leaves
       // and no copy may land after it: after a wait that gave up, the residual's boxes may be on their way
