@@ -368,6 +368,12 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         for (int64_t g = issued > kStages ? issued - kStages : 0; g < issued; ++g)
           while (!mbar_try(b_full + (uint32_t)(g % kStages) * 8, (uint32_t)(g / kStages) & 1) && clock64() - t0 < kWaitCycles) {
           }
+      } else if (!ok) {
+        // after a wait that gave up the leader may have stopped counting before this CTA's last
+        // copies: half a millisecond for them to land
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1 << 20)) {
+        }
       }
     } else if (rank == 0 && (warp == 1 || (warp == 3 && kParts > 1))) {
       // ----------------------------------------------------------- MMA issuers (leader), one a part
