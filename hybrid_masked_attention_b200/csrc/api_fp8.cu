@@ -18,6 +18,12 @@ bool mat_ok(const void* p, int32_t type, int64_t ld, int64_t rows, int64_t cols)
 bool scales_ok(const float* p, int64_t ld, int64_t rows, int64_t groups) {
   return p && aligned(p, 4) && (rows <= 1 || ld >= groups);
 }
+// An output in the place of an input: element for element, or a warp would write what another has
+// yet to read.
+bool in_place_ok(const void* out, int32_t out_type, int64_t ld_out, const void* in, int32_t in_type, int64_t ld_in,
+                 int64_t rows) {
+  return out != in || !out || (out_type == in_type && (rows <= 1 || ld_out == ld_in));
+}
 // The pitch of a single row is never used: one that suits every access.
 inline int64_t pitch(int64_t rows, int64_t ld, int64_t cols) { return rows <= 1 ? ceil_div(cols, 16) * 16 : ld; }
 
@@ -37,6 +43,9 @@ mtfm_status mtfm_add_rmsnorm_fp8(int32_t rows, int32_t dim, const void* d_x, int
   if (d_x_out && !mat_ok(d_x_out, x_type, ld_x_out, rows, dim)) return MTFM_ERR_INVALID_ARG;
   if (!d_out || (rows > 1 && ld_out < dim)) return MTFM_ERR_INVALID_ARG;
   if (!scales_ok(d_scale, ld_scale, rows, ceil_div(dim, kGroup)) || !aligned(d_rstd, 4)) return MTFM_ERR_INVALID_ARG;
+  if (!in_place_ok(d_x_out, x_type, ld_x_out, d_x, x_type, ldx, rows) ||
+      !in_place_ok(d_x_out, x_type, ld_x_out, d_delta, delta_type, ld_delta, rows))
+    return MTFM_ERR_INVALID_ARG;
   return cuda_status(launch_add_rmsnorm_fp8(
       nullptr, rows, dim, MatIn{d_x, pitch(rows, ldx, dim), x_type}, MatIn{d_delta, pitch(rows, ld_delta, dim), delta_type},
       rows, nullptr, d_w, eps > 0.f ? eps : kRmsEps, MatOut{d_x_out, pitch(rows, ld_x_out, dim), x_type},
@@ -62,6 +71,10 @@ mtfm_status mtfm_rmsnorm_bwd(int32_t rows, int32_t dim, const void* d_x, int32_t
     if (d_dres && !mat_ok(d_dres, dres_type, ld_dres, rows, dim)) return MTFM_ERR_INVALID_ARG;
     if (!d_ws || !aligned(d_ws, 16)) return MTFM_ERR_INVALID_ARG;
     if (ws_bytes < mtfm_rmsnorm_bwd_workspace_bytes(rows, dim)) return MTFM_ERR_WORKSPACE_TOO_SMALL;
+    if (!in_place_ok(d_dx, x_type, ld_dx, d_x, x_type, ldx, rows) ||
+        !in_place_ok(d_dx, x_type, ld_dx, d_dy, dy_type, ld_dy, rows) ||
+        !in_place_ok(d_dx, x_type, ld_dx, d_dres, dres_type, ld_dres, rows))
+      return MTFM_ERR_INVALID_ARG;
   }
   return cuda_status(launch_rmsnorm_bwd(
       rows, dim, MatIn{d_x, pitch(rows, ldx, dim), x_type}, d_w, d_rstd, MatIn{d_dy, pitch(rows, ld_dy, dim), dy_type},
@@ -99,7 +112,7 @@ mtfm_status mtfm_fp8_gemm(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, i
     return MTFM_ERR_INVALID_ARG;
   if (!mat_ok(d_out, out_type, ld_out, m, n) || (d_res && !mat_ok(d_res, out_type, ld_res, m, n)))
     return MTFM_ERR_INVALID_ARG;
-  if (d_res == d_out && m > 1 && ld_res != ld_out) return MTFM_ERR_INVALID_ARG;  // in place: the same rows
+  if (!in_place_ok(d_out, out_type, ld_out, d_res, out_type, ld_res, m)) return MTFM_ERR_INVALID_ARG;
   if (!d_status || !aligned(d_status, 4)) return MTFM_ERR_INVALID_ARG;
   const Fp8Epi epi{act, out_type, 1, {0, n, n, n, n}, {d_out, nullptr, nullptr, nullptr},
                    {pitch(m, ld_out, n), 0, 0, 0}, d_res, pitch(m, ld_res, n), nullptr};

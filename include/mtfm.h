@@ -421,6 +421,8 @@ mtfm_status mtfm_v2_target_layer_fwd(const mtfm_cfg* cfg, const void* d_meta, in
  * Columns between a row's end and its pitch are neither read nor written.  Pitches
  * and bases need the alignment of one element only, unless stated; rows that start
  * on 4-element boundaries (16 bytes for the product's output) take vector accesses.
+ * An output may stand in the place of an input where that is said, with the same type and
+ * pitch (refused otherwise); beyond that outputs overlap neither inputs nor one another.
  * Zero rows launch nothing (mtfm_rmsnorm_bwd still zeroes dw).  Sums and statistics
  * are fp32; results do not depend on timing (no atomics).
  * ------------------------------------------------------------------------- */
@@ -431,7 +433,7 @@ typedef enum { MTFM_ACT_NONE = 0, MTFM_ACT_SILU = 1 } mtfm_act;
  *   h = x + delta,  rstd = 1 / sqrt(mean(h^2) + eps),  (out, scale) = groups of h rstd w,
  *   x_out = h rounded to x's type (the norm takes h before that rounding).
  * x, x_out [rows, dim] (x_type); delta [rows, dim] or NULL (then x_out must be NULL);
- * x_out may be x itself, or NULL (the sum is not kept).  w fp32 [dim]; eps <= 0 selects
+ * x_out may be x itself, at its pitch, or NULL (the sum is not kept).  w fp32 [dim]; eps <= 0 selects
  * 1e-6; out [rows, dim]; scale [rows, ceil(dim / 128)]; rstd fp32 [rows] or NULL (what
  * the backward needs).  dim in [1, 16384]. */
 mtfm_status mtfm_add_rmsnorm_fp8(int32_t rows, int32_t dim, const void* d_x, int32_t x_type, int64_t ldx,
@@ -473,7 +475,7 @@ mtfm_status mtfm_fp8_quant(int32_t rows, int32_t cols, const void* d_x, int32_t 
  * act: MTFM_ACT_SILU to a relative (13 + 2 |x|) 2^-24 before the output's rounding (results
  * below 2^-119 in magnitude may be 0; NaN and minus infinity give NaN).
  * A and B: 16-byte aligned, pitches multiples of 16 (a single row may have any pitch).
- * out, res: out_type; res may be NULL, or out itself.  k >= 1.
+ * out, res: out_type; res may be NULL, or out itself, at its pitch.  k >= 1.
  * d_status: device word, zeroed once by the caller; a call on a word that is not zero does
  * nothing, and a device wait that gives up sets it.  mtfm_fp8_check synchronises `stream`
  * and returns what it says (MTFM_OK, MTFM_ERR_TIMEOUT, MTFM_ERR_BOUNDS). */
