@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import types
 from dataclasses import dataclass
 from typing import Optional
 
@@ -40,9 +41,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 try:
     from . import _fastcall
-except ImportError as e:
-    raise ImportError("_fastcall.so not found or not loadable; build it with "
-                      "`python hybrid_masked_attention_b200/build.py`") from e
+except ImportError:
+    _fastcall = None   # not built, or for another Python: the wrappers alone do all it does
 
 MTFM_OK = 0
 STATUS_NAMES = {
@@ -582,13 +582,21 @@ _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 _ACTS = {None: 0, "silu": 1}
 FP8_GROUP = 128
 
+# The current device and the raw current stream of a device; torch.cuda's own functions do the
+# same, 30 times as slowly in the stream's case, where torch has no such names.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
 # The wrappers below first offer a call to csrc/fastcall.c, which reads the same attributes,
 # makes the same checks and calls the entry point; it declines (None) whatever does not hold,
-# and the checks here then say what.
-_entry = lambda name: ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value
-_fastcall.setup(torch.float32, torch.bfloat16, _F8, torch.uint8, torch.int32, torch._C._cuda_getDevice,
-                torch._C._cuda_getCurrentRawStream, *map(_entry, (
-                    "mtfm_add_rmsnorm_fp8", "mtfm_rmsnorm_bwd", "mtfm_gate_fwd_fp8", "mtfm_fp8_quant", "mtfm_fp8_gemm")))
+# and the checks here then say what.  Without it every call goes through the checks here.
+_FAST = ("add_rmsnorm_fp8", "rmsnorm_bwd", "gate_fwd_fp8", "fp8_quant", "fp8_gemm")
+if _fastcall is not None:
+    _fastcall.setup(torch.float32, torch.bfloat16, _F8, torch.uint8, torch.int32, _current_device, _raw_stream,
+                    *(ctypes.cast(getattr(_lib, "mtfm_" + name), ctypes.c_void_p).value for name in _FAST))
+else:
+    _fastcall = types.SimpleNamespace(**{name: lambda *args: None for name in _FAST})
 
 
 def _groups(n: int) -> int:
@@ -630,12 +638,12 @@ def _device_of(t, name):
 def _run_on(dev, stream, where, fn, *args):
     """Calls fn(*args, stream) with device `dev` current; stream None: the device's current stream."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)   # torch.cuda.current_stream(dev).cuda_stream, 30 times as fast
+        raw = _raw_stream(dev)
     elif isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
         raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on device {dev}")
     else:
         raw = _stream(stream)
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):

@@ -1,0 +1,65 @@
+"""The 8-bit operators' Python wrappers with and without the marshalling in C (csrc/fastcall.c)."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+WITHOUT = "import sys; sys.path.insert(0, {root!r}); sys.modules['hybrid_masked_attention_b200._fastcall'] = None\n"
+
+
+def run(code, timeout=300):
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=timeout)
+    assert r.returncode == 0, (r.stdout + r.stderr)[-3000:]
+    return r.stdout
+
+
+def test_package_without_the_c_marshalling():
+    """The package imports, and its wrappers make their checks, without the extension and without
+    torch's internal names."""
+    out = run(WITHOUT.format(root=ROOT) + """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import hybrid_masked_attention_b200 as M
+x = torch.zeros(4, 64)
+q, s = x.to(torch.float8_e4m3fn), torch.zeros(4, 1)
+for call in (lambda: M.fp8_quant(x, q, s), lambda: M.add_rmsnorm_fp8(x, None, torch.ones(64), None, q, s),
+             lambda: M.fp8_gemm(q, s, q, s, x, torch.zeros(1, dtype=torch.int32))):
+    try:
+        call()
+    except ValueError as e:
+        assert "CUDA" in str(e)
+    else:
+        raise AssertionError("not refused")
+print("ok")
+""")
+    assert "ok" in out
+
+
+@pytest.mark.gpu
+def test_same_results_without_the_c_marshalling(cuda_ok):
+    code = """
+import hashlib
+import torch
+import hybrid_masked_attention_b200 as M
+F8 = torch.float8_e4m3fn
+g = torch.Generator(device="cuda").manual_seed(1)
+x, w = torch.randn(300, 256, generator=g, device="cuda"), torch.randn(256, generator=g, device="cuda")
+new = lambda r, c, t: torch.empty(r, c, dtype=t, device="cuda")
+q, s, rstd = new(300, 256, F8), new(300, 2, torch.float32), torch.empty(300, device="cuda")
+b, bs = new(256, 256, F8), new(2, 2, torch.float32)
+out, status = new(300, 256, torch.float32), torch.zeros(1, dtype=torch.int32, device="cuda")
+dx, dw = torch.empty_like(x), torch.empty_like(w)
+M.add_rmsnorm_fp8(x, None, w, None, q, s, rstd)
+M.fp8_quant(x[:256].contiguous(), b, bs, 128)
+M.fp8_gemm(q, s, b, bs, out, status, "silu")
+M.rmsnorm_bwd(x, w, rstd, out, None, dx, dw, torch.empty(M.rmsnorm_bwd_workspace_bytes(300, 256), dtype=torch.uint8, device="cuda"))
+M.fp8_check(status)
+print(hashlib.sha256(b"".join(t.cpu().contiguous().view(torch.uint8).numpy().tobytes() for t in (q, s, out, dx, dw))).hexdigest())
+"""
+    path = "import sys; sys.path.insert(0, {root!r})\n"
+    assert run(path.format(root=ROOT) + code) == run(WITHOUT.format(root=ROOT) + code)
