@@ -5,8 +5,8 @@
 Each .cu under csrc/ is compiled to an object in parallel with
 ``nvcc -gencode arch=compute_100a,code=sm_100a -lineinfo -O3``, then linked
 into ``hybrid_masked_attention_b200/libmtfm.so``; csrc/fastcall.c, the argument
-marshalling of the 8-bit operators, becomes ``_fastcall.so`` beside it (gcc, CPython's
-headers).  Rebuilds only when a source or header is newer than the library.
+marshalling of the 8-bit operators, becomes ``_fastcall.<ABI tag>.so`` beside it (gcc,
+CPython's headers; the package works without it, more slowly).  Rebuilds only when a source or header is newer than the library.
 
     python hybrid_masked_attention_b200/build.py --debug-bounds
 
@@ -31,7 +31,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmtfm.so")
-FASTCALL = os.path.join(PKG, "_fastcall.so")
+# named for the interpreter it is built with, so that another one passes it over
+FASTCALL = os.path.join(PKG, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 DEBUG_BUILD = os.path.join(PKG, "_build_debug_bounds")
 DEBUG_LIB = os.path.join(PKG, "libmtfm_debug_bounds.so")
 INCLUDE = os.path.join(ROOT, "include")
@@ -88,11 +89,17 @@ def build_fastcall(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"compiling {src} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, FASTCALL)
+    untagged = os.path.join(PKG, "_fastcall.so")   # an interpreter of any version would load it
+    if untagged != FASTCALL and os.path.exists(untagged):
+        os.remove(untagged)
     return FASTCALL
 
 
 def build(force: bool = False, verbose: bool = False, extra=(), debug_bounds: bool = False) -> str:
-    build_fastcall(force)
+    try:
+        build_fastcall(force)
+    except (RuntimeError, OSError) as e:   # no C compiler or no CPython headers
+        sys.stderr.write(f"argument marshalling in C left out, Python's is used: {e}\n")
     lib, build_dir = (DEBUG_LIB, DEBUG_BUILD) if debug_bounds else (LIB, BUILD)
     if debug_bounds:
         extra = (*extra, "-DMTFM_DEBUG_BOUNDS")

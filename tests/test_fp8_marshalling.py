@@ -2,10 +2,12 @@
 import os
 import subprocess
 import sys
+import sysconfig
 
 import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PKG = os.path.join(ROOT, "hybrid_masked_attention_b200")
 
 WITHOUT = "import sys; sys.path.insert(0, {root!r}); sys.modules['hybrid_masked_attention_b200._fastcall'] = None\n"
 
@@ -38,6 +40,18 @@ for call in (lambda: M.fp8_quant(x, q, s), lambda: M.add_rmsnorm_fp8(x, None, to
 print("ok")
 """)
     assert "ok" in out
+
+
+def test_extension_is_named_for_its_interpreter():
+    """Another interpreter must not load it: the file carries the ABI tag, and none without is left."""
+    sys.path.insert(0, PKG)
+    try:
+        import build
+    finally:
+        sys.path.remove(PKG)
+    build.build_fastcall()
+    assert build.FASTCALL.endswith(sysconfig.get_config_var("EXT_SUFFIX")) and os.path.exists(build.FASTCALL)
+    assert not os.path.exists(os.path.join(PKG, "_fastcall.so"))
 
 
 @pytest.mark.gpu
