@@ -120,7 +120,16 @@ static int stream_of(long dev, void** st) {
 }
 static int64_t groups(int64_t n) { return (n + 127) / 128; }
 static int fits(int64_t n) { return n >= 0 && n <= INT32_MAX; }
-static PyObject* done(mtfm_status s) { return PyLong_FromLong((long)s); }
+/* Returns the status of a call made without the interpreter's lock: a launch that waits for room
+ * in its queue must not stop the other threads, one of which the queue may be waiting for. */
+#define CALL(expr)             \
+  do {                         \
+    mtfm_status s_;            \
+    Py_BEGIN_ALLOW_THREADS     \
+    s_ = (expr);               \
+    Py_END_ALLOW_THREADS       \
+    return PyLong_FromLong(s_); \
+  } while (0)
 static PyObject* not_taken(void) {
   PyErr_Clear();
   Py_RETURN_NONE;
@@ -143,8 +152,8 @@ static PyObject* add_rmsnorm_fp8(PyObject* self, PyObject* const* a, Py_ssize_t 
       !mat(a[5], dev, d_f32, rows, groups(dim), &s) || (a[6] != Py_None && !vec_n(a[6], dev, d_f32, rows, &r)) ||
       !PyFloat_Check(a[7]) || !stream_of(dev, &st))
     return not_taken();
-  return done(p_mtfm_add_rmsnorm_fp8((int32_t)rows, (int32_t)dim, x.p, x.type, x.ld, d.p, d.type, d.ld, w,
-                                     (float)PyFloat_AS_DOUBLE(a[7]), xo.p, xo.ld, q.p, q.ld, s.p, s.ld, r, st));
+  CALL(p_mtfm_add_rmsnorm_fp8((int32_t)rows, (int32_t)dim, x.p, x.type, x.ld, d.p, d.type, d.ld, w,
+                              (float)PyFloat_AS_DOUBLE(a[7]), xo.p, xo.ld, q.p, q.ld, s.p, s.ld, r, st));
 }
 
 /* x, weight, rstd, dy, dres, dx, dw, ws */
@@ -159,8 +168,8 @@ static PyObject* rmsnorm_bwd(PyObject* self, PyObject* const* a, Py_ssize_t narg
       !opt_mat(a[4], dev, NULL, rows, dim, &dr) || !mat(a[5], dev, x.type ? d_bf16 : d_f32, rows, dim, &dx) ||
       !vec_n(a[6], dev, d_f32, dim, &dw) || !vec(a[7], dev, d_u8, &ws_bytes, &ws) || !stream_of(dev, &st))
     return not_taken();
-  return done(p_mtfm_rmsnorm_bwd((int32_t)rows, (int32_t)dim, x.p, x.type, x.ld, w, r, y.p, y.type, y.ld, dr.p, dr.type,
-                                 dr.ld, dx.p, dx.ld, dw, ws, (size_t)ws_bytes, st));
+  CALL(p_mtfm_rmsnorm_bwd((int32_t)rows, (int32_t)dim, x.p, x.type, x.ld, w, r, y.p, y.type, y.ld, dr.p, dr.type,
+                          dr.ld, dx.p, dx.ld, dw, ws, (size_t)ws_bytes, st));
 }
 
 /* cfg (address of an mtfm_cfg), meta, target, a, u, gamma, beta, out, scale, stats */
@@ -180,7 +189,7 @@ static PyObject* gate_fwd_fp8(PyObject* self, PyObject* const* a, Py_ssize_t nar
       !mat(a[7], dev, d_f8, rows, D, &q) || !mat(a[8], dev, d_f32, rows, groups(D), &s) ||
       !opt_packed(a[9], dev, d_f32, rows, 2, &ps) || !stream_of(dev, &st))
     return not_taken();
-  return done(p_mtfm_gate_fwd_fp8(cfg, meta, target, pa, pu, pg, pb, q.p, q.ld, s.p, s.ld, ps, st));
+  CALL(p_mtfm_gate_fwd_fp8(cfg, meta, target, pa, pu, pg, pb, q.p, q.ld, s.p, s.ld, ps, st));
 }
 
 /* x, out, scale, block_rows */
@@ -195,7 +204,7 @@ static PyObject* fp8_quant(PyObject* self, PyObject* const* a, Py_ssize_t nargs)
       !mat(a[1], dev, d_f8, rows, cols, &q) || !mat(a[2], dev, d_f32, (rows + br - 1) / br, groups(cols), &s) ||
       !stream_of(dev, &st))
     return not_taken();
-  return done(p_mtfm_fp8_quant((int32_t)rows, (int32_t)cols, x.p, x.type, x.ld, (int32_t)br, q.p, q.ld, s.p, s.ld, st));
+  CALL(p_mtfm_fp8_quant((int32_t)rows, (int32_t)cols, x.p, x.type, x.ld, (int32_t)br, q.p, q.ld, s.p, s.ld, st));
 }
 
 /* a, a_scale, b, b_scale, out, status, act (an mtfm_act), residual */
@@ -212,8 +221,8 @@ static PyObject* fp8_gemm(PyObject* self, PyObject* const* a, Py_ssize_t nargs) 
       !vec_n(a[5], dev, d_i32, 1, &status) || !opt_mat(a[7], dev, out.type ? d_bf16 : d_f32, m, n, &res) ||
       !stream_of(dev, &st))
     return not_taken();
-  return done(p_mtfm_fp8_gemm((int32_t)m, (int32_t)n, (int32_t)k, qa.p, qa.ld, sa.p, sa.ld, qb.p, qb.ld, sb.p, sb.ld,
-                              (int32_t)act, res.p, res.ld, out.p, out.type, out.ld, status, st));
+  CALL(p_mtfm_fp8_gemm((int32_t)m, (int32_t)n, (int32_t)k, qa.p, qa.ld, sa.p, sa.ld, qb.p, qb.ld, sb.p, sb.ld,
+                       (int32_t)act, res.p, res.ld, out.p, out.type, out.ld, status, st));
 }
 
 /* (fp32, bf16, e4m3, uint8, int32) dtypes, current device, raw current stream, entry addresses */

@@ -54,6 +54,46 @@ def test_extension_is_named_for_its_interpreter():
     assert not os.path.exists(os.path.join(PKG, "_fastcall.so"))
 
 
+def test_other_threads_run_while_an_entry_point_blocks():
+    """An entry point that blocks (libc's sleep in the place of the quantiser: its first argument
+    is the number of rows) does not hold the interpreter's lock."""
+    out = run("""
+import ctypes
+import sys
+import threading
+import time
+sys.path.insert(0, {pkg!r})
+import _fastcall
+f32, bf16, f8, u8, i32 = object(), object(), object(), object(), object()
+class Matrix:   # as much of a tensor on device 0 as the marshalling reads
+    def __init__(self, dtype, rows, cols):
+        self.dtype, self.shape = dtype, (rows, cols)
+    def get_device(self):
+        return 0
+    def stride(self):
+        return self.shape[1], 1
+    def data_ptr(self):
+        return 4096
+sleep = ctypes.cast(ctypes.CDLL(None).sleep, ctypes.c_void_p).value
+_fastcall.setup(f32, bf16, f8, u8, i32, lambda: 0, lambda dev: 0, *[sleep] * 5)
+ticks, end = [], threading.Event()
+def count():
+    while not end.is_set():
+        ticks.append(time.perf_counter())
+        time.sleep(0.01)
+t = threading.Thread(target=count)
+t.start()
+t0 = time.perf_counter()
+status = _fastcall.fp8_quant(Matrix(f32, 1, 128), Matrix(f8, 1, 128), Matrix(f32, 1, 1), 1)
+t1 = time.perf_counter()
+end.set()
+t.join()
+assert status == 0 and t1 - t0 > 0.9, (status, t1 - t0)
+print(sum(t0 + 0.2 < v < t1 - 0.2 for v in ticks))
+""".format(pkg=PKG))
+    assert int(out) >= 5
+
+
 @pytest.mark.gpu
 def test_same_results_without_the_c_marshalling(cuda_ok):
     code = """
