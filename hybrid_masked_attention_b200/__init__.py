@@ -795,13 +795,26 @@ class Fp8LayerWeights:
 
     @classmethod
     def quantized(cls, w: LayerWeights, stream=None) -> "Fp8LayerWeights":
-        """The 8-bit form of a layer's weights (the norms' parameters are shared)."""
+        """The 8-bit form of a layer's weights (the norms' parameters are shared).
+
+        The new tensors belong to the current stream.  On another ``stream`` the quantiser waits for
+        what the current one holds by then, which may still use their memory; the caller orders
+        later uses after ``stream``, as with any call on it."""
+        dev = w.w_in.device
+        side = stream if stream is None or isinstance(stream, torch.cuda.Stream) else \
+            torch.cuda.ExternalStream(_stream(stream), device=dev)
+        if side is not None:
+            side.wait_stream(torch.cuda.current_stream(dev))
+
         def q(t):
             if t is None:
                 return None
             out = torch.empty(t.shape, dtype=_F8, device=t.device)
             scale = torch.empty(_groups(t.shape[0]), _groups(t.shape[1]), dtype=_F32, device=t.device)
-            fp8_quant(t, out, scale, FP8_GROUP, stream)
+            fp8_quant(t, out, scale, FP8_GROUP, side)
+            if side is not None:   # not handed out again before the quantiser is done
+                out.record_stream(side)
+                scale.record_stream(side)
             return out, scale
         return cls(w.kind, w.rms_w, q(w.w_in), q(w.w_kv), q(w.w_o), w.gamma, w.beta)
 
