@@ -242,8 +242,8 @@ inline int dtype_size(int type) { return type == MTFM_BF16 ? 2 : 4; }
 
 // err (may be NULL): a device error word; the kernel does nothing while it is not zero.
 // With a row_map, rows from `mapped` on read row row_map[row - mapped] of x (a kernel of its own:
-// the test in the other one's loads cost it a third of its speed); delta and x_out must
-// then be NULL.
+// the test in the other one's loads cost it a third of its speed); x must then be fp32, delta and
+// x_out NULL.
 cudaError_t launch_add_rmsnorm_fp8(const int32_t* err, int rows, int dim, const MatIn& x, const MatIn& delta,
                                    int mapped, const int32_t* row_map, const float* w, float eps, const MatOut& x_out,
                                    const Fp8Out& out, float* rstd, cudaStream_t st);

@@ -198,7 +198,10 @@ cudaError_t types(const int32_t* err, int rows, int dim, const MatIn& x, const M
 
 template <typename XT, typename... Args>
 cudaError_t with_delta(const MatIn& delta, const int32_t* row_map, Args&&... args) {
-  if (row_map) return types<XT, Mapped>(args...);
+  if (row_map) {  // the layers' residual stream, which is fp32
+    if constexpr (std::is_same<XT, float>::value) return types<XT, Mapped>(args...);
+    else return cudaErrorInvalidValue;
+  }
   if (!delta.p) return types<XT, None>(args...);
   if (delta.type == MTFM_BF16) return types<XT, __nv_bfloat16>(args...);
   return types<XT, float>(args...);
