@@ -25,9 +25,11 @@
 // memory by the epilogue warps themselves, 32 rows a warp and each row in 4 warpgroups, they
 // cost 100 us of 560); warps 4..19 are the warpgroups, one TMEM lane (row) a thread.  Their 64
 // sums a thread take registers that the first four warps hand over (setmaxnreg).
-// What bounds it: at 8192^3 (511 us, 2.15 PFLOP/s) the hand-over of TMEM buffers, 820 cycles a block
-// where the tensor pipe needs 512; at 53133 x 1280 x 512 with SiLU (61 us) the epilogue, 2.5 of 4.4 us
-// a tile, which only two blocks of the next tile overlap.
+// What bounds it: at 8192^3 (523 us alone, 595 in a loop under the power
+// cap) the hand-over of TMEM buffers, 950 cycles a block as the epilogue's warps count them where the
+// tensor pipe needs 512 (it is active for 0.60 of the time, the issue slots for 0.74); at 53133 x 1280
+// x 512 with SiLU (75 to 78 us) instruction issue (0.72): a tile's four blocks take 3700 cycles, SiLU
+// and the store 3600, which only two blocks of the next tile overlap.
 //
 // Every wait is bounded; a wait that gives up raises its CTA's abort flag, the other CTA's own
 // waits then run out too, both meet at the cluster barrier, and the error word gets the
@@ -77,7 +79,9 @@ constexpr uint32_t stage_bytes_g() { return kABytes + (uint32_t)(BN / 2) * kGrou
 //   kOutStaged : with a row map: staged, then each warp adds the residual to, and stores, whole
 //                128-byte pieces of rows (a thread's own row, from its registers, would touch 32
 //                rows at a time: 4911 x 1000 x 1000 took 40 us that way and 23 this way).
-//   kOutDirect : rows that do not start, or whose end does not fall, on 16-byte boundaries.
+//   kOutDirect : rows that do not start, or whose end does not fall, on 16-byte boundaries
+//                (4911 x 1001 x 1000, fp32 / bf16: 43 / 68 us, 82 / 83 with a residual, where 1000
+//                columns take 15 / 14 and 20 / 15).
 constexpr int kOutTma = 0, kOutStaged = 1, kOutDirect = 2, kOutTmaRes = 3;
 template <int BN, int OUT>
 constexpr int stages_g() { return BN == 256 ? 5 : OUT == kOutTmaRes ? 4 : 6; }

@@ -9,7 +9,8 @@
 // block's scales, to fp32 registers.  The cluster's partial sums meet in shared memory: CTA q
 // receives every CTA's sums of BT / S rows of A, adds them in the order of the depth, so that
 // the result does not depend on timing, and finishes those rows.
-// 1 x 8192 x 4096: 7.6 us a call back to back, 4.4 TB/s of B (256 CTAs of 8 blocks).
+// 1 x 8192 x 4096 on the device: 6.8 us with B in L2, 9.0 us from HBM (3.7 TB/s; 256 CTAs of 8
+// blocks).
 #include <algorithm>
 
 #include "gemm_fp8.cuh"
@@ -328,7 +329,10 @@ cudaError_t go(const RowArgs& args, const Fp8In& a, const Fp8In& b, cudaStream_t
 
 template <int BT, typename OT>
 cudaError_t by_split(const RowArgs& args, const Fp8In& a, const Fp8In& b, cudaStream_t st) {
-  // split the depth until there are three CTAs for two SMs, as long as each keeps a block
+  // split the depth until there are three CTAs for two SMs, as long as each keeps a block.  Splits
+  // of 1 / 2 / 4 (/ 8), us on the device, B from HBM: N 8192, K 4096 (4 taken) 11.4 / 9.3 / 9.0 with
+  // one row and 15.7 / 12.3 / 10.9 with 32; N 2048, K 1024 (8 taken) 4.7 / 4.4 / 3.7 / 3.6 and 7.8 /
+  // 6.5 / 5.2 / 4.8; N 1024, K 512 (4 taken) 3.3 / 3.6 / 3.3 and 6.4 / 5.4 / 4.6.
   const int64_t nN = ((int64_t)args.N + kRows - 1) / kRows;
   const int nK = (args.K + kGroup - 1) / kGroup;
   int S = 1;
@@ -348,8 +352,10 @@ cudaError_t by_rows(const RowArgs& args, const Fp8In& a, const Fp8In& b, cudaStr
 
 }  // namespace
 
-// Up to 32 rows: at N 8192, K 4096 this kernel takes 11 us (16 rows) and 14 (32) against 18 of the
-// pairs' tiles, which waste what is missing to 256 rows but read B as fast from 33 rows on.
+// Up to 32 rows, on the device with B from HBM: at N 8192, K 4096 this kernel takes 9.7 us (16 rows)
+// and 10.9 (32) against 17.4 and 15.2 of the pairs' tiles, at N 1024, K 512 3.6 and 4.6 against 5.4.
+// From 33 rows on the pairs take over, 15.2 us there for up to 64 rows and 15.7 for 128: a thread here
+// would need that many sums.
 bool gemm_fp8_rows_takes(int M, int N, int K) {
   const int64_t nN = ((int64_t)N + kRows - 1) / kRows;
   return M <= 32 && K <= kMaxBlocks * kMaxSplit * kGroup && nN * kMaxSplit < (1ll << 31);

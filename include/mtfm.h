@@ -431,7 +431,7 @@ typedef enum { MTFM_ACT_NONE = 0, MTFM_ACT_SILU = 1 } mtfm_act;
 
 /* Residual addition, RMSNorm and quantisation in one pass:
  *   h = x + delta,  rstd = 1 / sqrt(mean(h^2) + eps),  (out, scale) = groups of h rstd w,
- *   x_out = h rounded to x's type (the norm takes h before that rounding).
+ *   x_out = h rounded to x's type (the norm takes h before that rounding, rstd and scale with it).
  * x, x_out [rows, dim] (x_type); delta [rows, dim] or NULL (then x_out must be NULL);
  * x_out may be x itself, at its pitch, or NULL (the sum is not kept).  w fp32 [dim]; eps <= 0 selects
  * 1e-6; out [rows, dim]; scale [rows, ceil(dim / 128)]; rstd fp32 [rows] or NULL (what
@@ -443,8 +443,9 @@ mtfm_status mtfm_add_rmsnorm_fp8(int32_t rows, int32_t dim, const void* d_x, int
 
 /* Backward of the norm (the quantisation passes gradients through unchanged):
  *   g = dy w,  dx = rstd (g - x rstd^2 mean(g x)) + dres,  dw = sum over rows of dy x rstd.
- * x: the stream the forward normalised (its x_out, or x where delta was NULL); dx is the
- * gradient of it, and so of both x and delta.  dres: gradient arriving along the residual
+ * x: the forward's x_out (or x where delta was NULL): for a bf16 stream with a delta that is h
+ * rounded to bf16, and the gradients are those of the norm at that value; dx is the gradient of
+ * it, and so of both x and delta.  dres: gradient arriving along the residual
  * stream, or NULL.  dy, dres: their own types; dx: x's type, and may be dy or dres where
  * type and pitch agree.  dw fp32 [dim], overwritten.  d_ws: at least
  * mtfm_rmsnorm_bwd_workspace_bytes(rows, dim) bytes, 16-byte aligned, not shared by calls
@@ -471,7 +472,9 @@ mtfm_status mtfm_fp8_quant(int32_t rows, int32_t cols, const void* d_x, int32_t 
 /* Block-scaled product: out[m, n] = act(sum_k A[m, k] B[n, k]) + res[m, n], with A [m, k] in
  * 1 x 128 groups and B [n, k] in 128 x 128 blocks (a weight, "out x in"; the gradient
  * dX = dY W is the same call on quantised dY and on the quantised transpose of W).
- * Products of one 128-deep block are summed by the tensor cores, scaled, and added in fp32.
+ * Products of one 128-deep block are summed by the tensor cores, scaled, and added in fp32; the
+ * scale of a block, A's times B's, is itself an fp32 number (past 2^128 it is infinite, and below
+ * 2^-126 it loses bits).
  * act: MTFM_ACT_SILU to a relative (13 + 2 |x|) 2^-24 before the output's rounding (results
  * below 2^-119 in magnitude may be 0; NaN and minus infinity give NaN).
  * A and B: 16-byte aligned, pitches multiples of 16 (a single row may have any pitch).
