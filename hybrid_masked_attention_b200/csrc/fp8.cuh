@@ -185,7 +185,7 @@ __device__ __forceinline__ void put4_e4m3(uint8_t* p, int lane, int n, const flo
 
 // The factor of a group, 448 (1 / m): reciprocal and product each rounded to nearest, which is
 // what `448.0 / m` is in torch, so that the quantiser's bytes are those of the plain form.  (With
-// an approximate reciprocal one value in 10^5 or so fell on the other side of a rounding border.)
+// an approximate reciprocal single values fell on the other side of a rounding border.)
 __device__ __forceinline__ float quant_factor(float m) { return kE4m3Max * __frcp_rn(m); }
 
 // Quantises the warp's C neighbouring 128-column groups of a row, of which n columns are left
